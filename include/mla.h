@@ -21,7 +21,10 @@
  * openarchlab DeepSeek-V4.1-Flash page "4A · Multi-head Latent Attention"
  * (§1 Định nghĩa, §2 Luồng, §4 Profiling); the grouped output projection that
  * follows it there (§2 Luồng, §3 W_O nhóm) is mla_group_wo. The step before
- * the decode, writing a new token into its cache slot, is mla_cache_append.
+ * the decode, writing a new token into its cache slot, is mla_cache_append;
+ * mla_rope_append is that step on raw projection outputs, mla_prefix_decode the
+ * decode of a batch that shares a prefix, mla_fp4_linear a projection whose
+ * weights are FP4 entries.
  *
  * Conventions for every call:
  *  - Tensor pointers are DEVICE pointers owned by the caller. The library
@@ -39,7 +42,8 @@
  *  - Device pointers must be 16-byte aligned.
  *  - Supported shapes (decode, projections, combine, append): Ckv = 512; Dr
  *    in {0 (shared-latent variant), 32, 64}; Dn in {64, 128}; Vd = 128; H a
- *    multiple of 8, at most 128; Q in [1, 4]. mla_group_wo states its own.
+ *    multiple of 8, at most 128; Q in [1, 4]. mla_group_wo, mla_rope_append,
+ *    mla_prefix_decode and mla_fp4_linear state their own.
  *    Anything else returns MLA_ERR_UNSUPPORTED.
  */
 #ifndef LATENT_KV_DECODE_MLA_H
@@ -327,6 +331,174 @@ typedef struct mla_group_wo_args {
 size_t mla_group_wo_workspace_size(const mla_group_wo_args* a);
 mla_status_t mla_group_wo(const mla_group_wo_args* a, void* workspace, size_t workspace_bytes,
                           void* stream);
+
+/*
+ * mla_rope_append - the append of a whole step or prompt with the position
+ * rotation on the way: new latent rows are copied into the cache, the new
+ * rope rows are rotated at their positions and stored, and the queries'
+ * position parts are rotated by the same angles. mla_cache_append copies rope
+ * rows that arrive rotated; this call takes the projections' raw outputs.
+ *
+ *   Tokens: N new tokens in rows of c_kv, k_pe and q_pe, in sequence order.
+ *     cu_tokens == NULL: sequence b owns rows [b*Q, (b+1)*Q), N = B*Q.
+ *     cu_tokens (B+1) int32, non-decreasing: sequence b owns rows
+ *     [cu_tokens[b], cu_tokens[b+1]) (none is allowed); rows outside
+ *     [cu_tokens[0], cu_tokens[B]) belong to no sequence: nothing is read
+ *     from or written for them. Q is then ignored.
+ *   seq_lens (B) int32, required: the lengths AFTER the append. The i-th of a
+ *     sequence's n new tokens is token t = seq_lens[b] - n + i and goes to the
+ *     row mla_decode reads for t (kv_cache / pe_cache, strides, Lk,
+ *     block_table, page_size as there).
+ *   Rotation: position pos_offset + t (pos_offset = the length of a shared
+ *     prefix stored elsewhere, else 0); pair (2j, 2j+1) of the Dr dims turns by
+ *     pos * rope_theta^(-2j/Dr).
+ *   c_kv row n at c_kv + n*c_kv_stride, k_pe row n at k_pe + n*k_pe_stride.
+ *   q_pe (or NULL with H = 0): head h of row n at q_pe + n*q_token_stride +
+ *     h*q_head_stride; its rotation goes to q_out + n*o_token_stride +
+ *     h*o_head_stride with cu_tokens, and to q_out + (n/Q)*o_batch_stride +
+ *     (n%Q)*o_token_stride + h*o_head_stride without (mla_decode's (B,H,Q,Dr)
+ *     has strides H*Q*Dr, Dr, Q*Dr). q_out may be q_pe with the same strides;
+ *     other overlaps of inputs and outputs are not allowed. Strides are in
+ *     elements; pointers need the alignment of an element, and 16-byte
+ *     aligned rows take the wide path.
+ *   dtype: MLA_F32 or MLA_BF16, of every tensor. Ckv = 512; Dr 32 or 64; any H
+ *     up to 1024.
+ *   err_flag: optional device int32; a token with t outside [0, Lk) or a page
+ *     id outside [0, num_pages) sets MLA_DEVICE_ERR_BLOCK_TABLE and is not
+ *     written to the cache (its queries are still rotated).
+ */
+typedef struct mla_rope_append_args {
+  int B, Q, N;
+  int Ckv, Dr, H;
+  mla_dtype_t dtype;       /* MLA_F32 or MLA_BF16 */
+  const void* c_kv;
+  const void* k_pe;
+  const void* q_pe;        /* or NULL (H = 0) */
+  void* q_out;             /* or NULL (H = 0) */
+  int64_t c_kv_stride, k_pe_stride;
+  int64_t q_token_stride, q_head_stride;
+  int64_t o_batch_stride, o_token_stride, o_head_stride;
+  void* kv_cache;
+  void* pe_cache;
+  int64_t kv_row_stride, pe_row_stride;
+  int64_t kv_batch_stride, pe_batch_stride;  /* contiguous layout only */
+  int Lk;                  /* contiguous: rows per sequence; paged: max_pages*page_size */
+  const int32_t* seq_lens; /* (B), lengths after the append */
+  const int32_t* block_table; /* (B,max_pages) or NULL */
+  int max_pages, page_size, num_pages;
+  const int32_t* cu_tokens; /* (B+1) or NULL */
+  int pos_offset;
+  float rope_theta;
+  int32_t* err_flag;       /* optional device status word */
+} mla_rope_append_args;
+
+mla_status_t mla_rope_append(const mla_rope_append_args* a, void* stream);
+
+/*
+ * mla_prefix_decode - mla_decode for a batch whose sequences all begin with
+ * the same prefix, stored once:
+ *
+ *   logit = (q_lat . c[t] + q_pe . r[t]) * softmax_scale over the prefix's
+ *           tokens, then over the sequence's own
+ *   x     = softmax(logit) . c,  lse = log sum exp(logit)
+ *
+ * The rows of all sequences are stacked, so the prefix is read once per 128
+ * of them, whatever the number of heads per sequence.
+ *
+ *   q_lat (B,H,Q,Ckv), q_pe (B,H,Q,Dr), x (B,H,Q,Ckv), lse (B,H,Q) as for
+ *     mla_decode, in dtype (lse float32).
+ *   Prefix: prefix_len tokens (0 allowed). prefix_table == NULL: token t is row
+ *     t of prefix_kv / prefix_pe (row strides in elements). Else token t is row
+ *     prefix_table[t/page_size]*page_size + t%page_size of pools of
+ *     prefix_num_pages pages; the table holds ceil(prefix_len/page_size) ids.
+ *   Own tokens: kv_cache / pe_cache, strides, Lk, seq_lens, block_table,
+ *     max_pages, num_pages as for mla_decode; they count the tokens behind the
+ *     prefix, so token t of a sequence is at position prefix_len + t. Lk = 0
+ *     (no own tokens; kv_cache may be NULL) and lengths of 0 are allowed.
+ *     page_size is that of both tables. The two storages may share a pool.
+ *   Visibility: t < length; causal_mask[position] != 0 when causal_mask
+ *     (prefix_len + Lk) is given; when causal is non-zero, position <=
+ *     prefix_len + len_b - Q + q. A row that sees nothing gets x = 0 and
+ *     lse = -inf (+ the sink). Cache rows that no query may see (behind a
+ *     sequence's end, masked by causal_mask, on a bad page) may hold
+ *     anything, NaN included.
+ *   sinks: as for mla_decode.
+ *   Supported: MLA_F32 or MLA_BF16; Ckv = 512; Dr 0, 32 or 64; H a multiple of 8
+ *     up to 128, Q 1..4. bf16 with contiguous storage or pages of a
+ *     multiple of 64 rows runs on the tensor cores; everything else in float32
+ *     on the CUDA cores.
+ *   num_splits: 0 = auto; each block of stacked rows cuts its tokens into this
+ *     many ranges, and the call then merges the partial results itself (no
+ *     mla_combine): x and lse are final when the enqueued work completes.
+ *   workspace: mla_prefix_decode_workspace_size(a) bytes, 256-byte aligned
+ *     (may be NULL when that is 0). It is written before it is read in every call.
+ *   err_flag: as for mla_decode.
+ */
+typedef struct mla_prefix_args {
+  int B, H, Q;
+  int Ckv, Dr;
+  mla_dtype_t dtype;
+  const void* q_lat;
+  const void* q_pe;
+  const void* prefix_kv;
+  const void* prefix_pe;
+  int64_t prefix_kv_stride, prefix_pe_stride;
+  int prefix_len;
+  const int32_t* prefix_table; /* (ceil(prefix_len/page_size)) or NULL */
+  int prefix_num_pages;
+  const void* kv_cache;
+  const void* pe_cache;
+  int64_t kv_row_stride, pe_row_stride;
+  int64_t kv_batch_stride, pe_batch_stride;  /* contiguous layout only */
+  int Lk;
+  const int32_t* seq_lens;    /* (B) or NULL */
+  const int32_t* block_table; /* (B,max_pages) or NULL */
+  int max_pages, page_size, num_pages;
+  const uint8_t* causal_mask; /* (prefix_len + Lk) or NULL */
+  int causal;
+  float softmax_scale;
+  const float* sinks;         /* (H) or NULL */
+  int num_splits;             /* 0 = auto */
+  void* x;
+  float* lse;                 /* or NULL */
+  int32_t* err_flag;          /* optional device status word */
+} mla_prefix_args;
+
+int mla_prefix_decode_num_splits(const mla_prefix_args* a);
+size_t mla_prefix_decode_workspace_size(const mla_prefix_args* a);
+mla_status_t mla_prefix_decode(const mla_prefix_args* a, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/*
+ * mla_fp4_linear - products of few tokens with weights held in the cache's FP4
+ * entries (E2M1 codes, an E4M3 scale per 16 channels):
+ *
+ *   out[t, g*N + n] = scale * sum_k x_g[t, k] * W[g, n, k],   t = b*Q + q
+ *
+ *   w   (G, N, K/512) entries of 288 bytes, packed: entry i of a row holds
+ *       channels 512 i .. 512 i + 511 in the layout mla_decode reads.
+ *       mla_cache_append with rope_tail = 0 writes such rows.
+ *   x   bf16; channel k of group g of token (b, q) at x + b*x_batch_stride +
+ *       q*x_token_stride + g*x_group_stride + (k/512)*x_block_stride + k%512,
+ *       strides in elements, multiples of 8 (x (B,H,Q,512) with H/G heads per
+ *       group: strides H*Q*512, 512, (H/G)*Q*512, Q*512).
+ *   out (B*Q, G*N) bf16, packed. Products and sums are float32, rounded once.
+ *   K a multiple of 512; any B, Q, G, N. x and w 16-byte aligned.
+ *   workspace: mla_fp4_linear_workspace_size(a) bytes, 256-byte aligned (may
+ *       be NULL when that is 0). It is written before it is read in every call.
+ */
+typedef struct mla_fp4_linear_args {
+  int B, Q, G, N, K;
+  const void* x;
+  int64_t x_batch_stride, x_token_stride, x_group_stride, x_block_stride;
+  const void* w;
+  float scale;
+  void* out;
+} mla_fp4_linear_args;
+
+size_t mla_fp4_linear_workspace_size(const mla_fp4_linear_args* a);
+mla_status_t mla_fp4_linear(const mla_fp4_linear_args* a, void* workspace, size_t workspace_bytes,
+                            void* stream);
 
 #ifdef __cplusplus
 }

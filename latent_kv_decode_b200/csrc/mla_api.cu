@@ -5,11 +5,15 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #include "append.h"
 #include "common.cuh"
+#include "fp4_linear.h"
 #include "launch.h"
+#include "prefix.h"
+#include "rope_append.h"
 
 namespace {
 
@@ -394,4 +398,216 @@ extern "C" mla_status_t mla_group_wo(const mla_group_wo_args* a, void* workspace
   const size_t need = mla::group_wo_workspace_bytes(a, sm_count());
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return MLA_ERR_WORKSPACE;
   return cuda_status(mla::launch_group_wo_sm100(a, workspace, sm_count(), (cudaStream_t)stream));
+}
+
+// ---------------------------------------------------------------------------
+// rotating cache append
+// ---------------------------------------------------------------------------
+namespace {
+
+mla_status_t validate_rope_append(const mla_rope_append_args* a) {
+  if (!a) return MLA_ERR_INVALID_ARG;
+  if (a->B <= 0 || a->N < 0 || a->Lk <= 0 || a->Ckv <= 0 || a->Dr <= 0 || a->H < 0) return MLA_ERR_INVALID_ARG;
+  if (!a->cu_tokens && (a->Q <= 0 || (int64_t)a->B * a->Q != a->N)) return MLA_ERR_INVALID_ARG;
+  if (a->dtype != MLA_F32 && a->dtype != MLA_BF16) return MLA_ERR_UNSUPPORTED;
+  if (a->Ckv != mla::kCkv || (a->Dr != 32 && a->Dr != 64) || a->H > 1024) return MLA_ERR_UNSUPPORTED;
+  if (!(a->rope_theta > 0.f) || !isfinite(a->rope_theta)) return MLA_ERR_INVALID_ARG;
+  if (!a->kv_cache || !a->pe_cache || !a->seq_lens) return MLA_ERR_INVALID_ARG;
+  if (a->N > 0 && (!a->c_kv || !a->k_pe || (a->H > 0 && (!a->q_pe || !a->q_out)))) return MLA_ERR_INVALID_ARG;
+  const int64_t esz = a->dtype == MLA_F32 ? 4 : 2;
+  for (const void* p : {a->c_kv, a->k_pe, (const void*)a->kv_cache, (const void*)a->pe_cache,
+                        a->H > 0 ? a->q_pe : nullptr, a->H > 0 ? (const void*)a->q_out : nullptr})
+    if (!aligned(p, esz)) return MLA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)a->seq_lens, (const void*)a->block_table, (const void*)a->cu_tokens,
+                        (const void*)a->err_flag})
+    if (!aligned(p, 4)) return MLA_ERR_INVALID_ARG;
+  if (a->c_kv_stride < 0 || a->k_pe_stride < 0) return MLA_ERR_INVALID_ARG;
+  if (a->kv_row_stride < a->Ckv || a->pe_row_stride < a->Dr) return MLA_ERR_INVALID_ARG;
+  if (a->block_table) {
+    if (a->page_size <= 0 || a->max_pages <= 0 || a->num_pages <= 0) return MLA_ERR_INVALID_ARG;
+    if ((int64_t)a->max_pages * a->page_size < a->Lk) return MLA_ERR_INVALID_ARG;
+  } else if (a->B > 1) {
+    // cache rows of two sequences, or of two tokens, may interleave (a combined
+    // row) but not coincide
+    if (a->kv_batch_stride < (int64_t)a->Lk * a->kv_row_stride) return MLA_ERR_INVALID_ARG;
+    if (a->pe_batch_stride < (int64_t)a->Lk * a->pe_row_stride) return MLA_ERR_INVALID_ARG;
+  }
+  if (a->H > 0 && a->N > 0) {
+    // two heads' or tokens' outputs must not coincide
+    if (a->H > 1 && a->o_head_stride < a->Dr) return MLA_ERR_INVALID_ARG;
+    const bool many = a->cu_tokens ? a->N > 1 : a->Q > 1;
+    if (many && a->o_token_stride < a->Dr) return MLA_ERR_INVALID_ARG;
+    if (!a->cu_tokens && a->B > 1 && a->o_batch_stride < a->Dr) return MLA_ERR_INVALID_ARG;
+  }
+  return MLA_OK;
+}
+
+}  // namespace
+
+extern "C" mla_status_t mla_rope_append(const mla_rope_append_args* a, void* stream) {
+  mla_status_t s = validate_rope_append(a);
+  if (s != MLA_OK) return s;
+  return cuda_status(mla::launch_rope_append(a, (cudaStream_t)stream));
+}
+
+// ---------------------------------------------------------------------------
+// shared-prefix decode
+// ---------------------------------------------------------------------------
+namespace {
+
+mla_status_t validate_prefix(const mla_prefix_args* a) {
+  if (!a) return MLA_ERR_INVALID_ARG;
+  if (a->B <= 0 || a->H <= 0 || a->Q <= 0 || a->prefix_len < 0 || a->Lk < 0) return MLA_ERR_INVALID_ARG;
+  if (a->dtype != MLA_F32 && a->dtype != MLA_BF16) return MLA_ERR_UNSUPPORTED;
+  if (a->Ckv != mla::kCkv || !(a->Dr == 0 || a->Dr == 32 || a->Dr == 64)) return MLA_ERR_UNSUPPORTED;
+  if (a->H < 8 || a->H > 128 || a->H % 8 != 0 || a->Q > 4) return MLA_ERR_UNSUPPORTED;
+  // stacked rows and positions are 32-bit
+  if ((int64_t)a->B * a->H * a->Q > (1 << 30) || (int64_t)a->prefix_len + a->Lk > (1 << 30))
+    return MLA_ERR_UNSUPPORTED;
+  if (a->num_splits < 0 || a->num_splits > kMaxSplits) return MLA_ERR_INVALID_ARG;
+  if (!a->q_lat || !a->x || (a->Dr > 0 && !a->q_pe)) return MLA_ERR_INVALID_ARG;
+  if (a->prefix_len > 0 && (!a->prefix_kv || (a->Dr > 0 && !a->prefix_pe))) return MLA_ERR_INVALID_ARG;
+  if (a->Lk > 0 && (!a->kv_cache || (a->Dr > 0 && !a->pe_cache))) return MLA_ERR_INVALID_ARG;
+  for (const void* p : {a->q_lat, a->Dr > 0 ? a->q_pe : nullptr, a->prefix_kv, a->Dr > 0 ? a->prefix_pe : nullptr,
+                        a->kv_cache, a->Dr > 0 ? a->pe_cache : nullptr, (const void*)a->x})
+    if (!aligned(p, 16)) return MLA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)a->prefix_table, (const void*)a->seq_lens, (const void*)a->block_table,
+                        (const void*)a->sinks, (const void*)a->lse, (const void*)a->err_flag})
+    if (!aligned(p, 4)) return MLA_ERR_INVALID_ARG;
+  const int64_t esz = a->dtype == MLA_F32 ? 4 : 2;
+  auto rows_ok = [&](int64_t kv, int64_t pe) {
+    return kv >= a->Ckv && (kv * esz) % 16 == 0 && (a->Dr == 0 || (pe >= a->Dr && (pe * esz) % 16 == 0));
+  };
+  if (a->prefix_len > 0) {
+    if (!rows_ok(a->prefix_kv_stride, a->prefix_pe_stride)) return MLA_ERR_INVALID_ARG;
+    if (a->prefix_table && (a->page_size <= 0 || a->prefix_num_pages <= 0)) return MLA_ERR_INVALID_ARG;
+  }
+  if (a->Lk > 0) {
+    if (!rows_ok(a->kv_row_stride, a->pe_row_stride)) return MLA_ERR_INVALID_ARG;
+    if (a->block_table) {
+      if (a->page_size <= 0 || a->max_pages <= 0 || a->num_pages <= 0) return MLA_ERR_INVALID_ARG;
+      if ((int64_t)a->max_pages * a->page_size < a->Lk) return MLA_ERR_INVALID_ARG;
+    } else if (a->B > 1) {
+      if (a->kv_batch_stride < (int64_t)a->Lk * a->kv_row_stride || (a->kv_batch_stride * esz) % 16 != 0)
+        return MLA_ERR_INVALID_ARG;
+      if (a->Dr > 0 && (a->pe_batch_stride < (int64_t)a->Lk * a->pe_row_stride || (a->pe_batch_stride * esz) % 16 != 0))
+        return MLA_ERR_INVALID_ARG;
+    }
+  }
+  if (!(a->softmax_scale > 0.f) || !isfinite(a->softmax_scale)) return MLA_ERR_INVALID_ARG;
+  return MLA_OK;
+}
+
+int prefix_splits(const mla_prefix_args* a) {
+  if (a->num_splits > 0) return a->num_splits;
+  return mla::prefix_simt_auto_splits(a, sm_count());
+}
+
+size_t prefix_ws_o_bytes(const mla_prefix_args* a, int S) {
+  return ((size_t)S * a->B * a->H * a->Q * a->Ckv * sizeof(float) + 255) & ~(size_t)255;
+}
+
+size_t prefix_ws_bytes(const mla_prefix_args* a, int S) {
+  return S <= 1 ? 0 : prefix_ws_o_bytes(a, S) + (size_t)S * a->B * a->H * a->Q * sizeof(float);
+}
+
+}  // namespace
+
+extern "C" int mla_prefix_decode_num_splits(const mla_prefix_args* a) {
+  return validate_prefix(a) != MLA_OK ? -1 : prefix_splits(a);
+}
+
+extern "C" size_t mla_prefix_decode_workspace_size(const mla_prefix_args* a) {
+  return validate_prefix(a) != MLA_OK ? 0 : prefix_ws_bytes(a, prefix_splits(a));
+}
+
+extern "C" mla_status_t mla_prefix_decode(const mla_prefix_args* a, void* workspace, size_t workspace_bytes,
+                                          void* stream) {
+  mla_status_t s = validate_prefix(a);
+  if (s != MLA_OK) return s;
+  const int S = prefix_splits(a);
+  const size_t need = prefix_ws_bytes(a, S);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return MLA_ERR_WORKSPACE;
+  mla::PrefixParams p;
+  memset(&p, 0, sizeof(p));
+  p.B = a->B;
+  p.H = a->H;
+  p.Q = a->Q;
+  p.HQ = a->H * a->Q;
+  p.Ckv = a->Ckv;
+  p.Dr = a->Dr;
+  p.D = a->Ckv + a->Dr;
+  p.N = a->B * a->H * a->Q;
+  p.q_lat = a->q_lat;
+  p.q_pe = a->q_pe;
+  p.pkv = a->prefix_kv;
+  p.ppe = a->prefix_pe;
+  p.pkv_row = a->prefix_kv_stride;
+  p.ppe_row = a->prefix_pe_stride;
+  p.Lp = a->prefix_len;
+  p.ptable = a->prefix_table;
+  p.p_pages = a->prefix_num_pages;
+  p.kv = a->kv_cache;
+  p.pe = a->pe_cache;
+  p.kv_row = a->kv_row_stride;
+  p.pe_row = a->pe_row_stride;
+  p.kv_batch = a->kv_batch_stride;
+  p.pe_batch = a->pe_batch_stride;
+  p.Lk = a->Lk;
+  p.seq_lens = a->seq_lens;
+  p.table = a->block_table;
+  p.max_pages = a->max_pages;
+  p.page_size = a->page_size;
+  p.num_pages = a->num_pages;
+  p.mask = a->causal_mask;
+  p.causal = a->causal;
+  p.scale = a->softmax_scale;
+  p.sinks = a->sinks;
+  p.num_splits = S;
+  p.x = a->x;
+  p.lse = a->lse;
+  p.err = a->err_flag;
+  if (S > 1) {
+    p.ws_o = (float*)workspace;
+    p.ws_lse = (float*)((char*)workspace + prefix_ws_o_bytes(a, S));
+  }
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool bf16 = a->dtype == MLA_BF16;
+  s = cuda_status(mla::launch_prefix_simt(p, bf16, st));
+  if (s != MLA_OK || S == 1) return s;
+  return cuda_status(mla::launch_prefix_combine(p, bf16, st));
+}
+
+// ---------------------------------------------------------------------------
+// products with FP4 weights
+// ---------------------------------------------------------------------------
+namespace {
+
+mla_status_t validate_fp4_linear(const mla_fp4_linear_args* a) {
+  if (!a) return MLA_ERR_INVALID_ARG;
+  if (a->B <= 0 || a->Q <= 0 || a->G <= 0 || a->N <= 0 || a->K <= 0) return MLA_ERR_INVALID_ARG;
+  if (!a->x || !a->w || !a->out) return MLA_ERR_INVALID_ARG;
+  if (!aligned(a->x, 16) || !aligned(a->w, 16) || !aligned(a->out, 4)) return MLA_ERR_INVALID_ARG;
+  if (!isfinite(a->scale)) return MLA_ERR_INVALID_ARG;
+  for (int64_t s : {a->x_batch_stride, a->x_token_stride, a->x_group_stride, a->x_block_stride})
+    if (s < 0 || s % 8 != 0) return MLA_ERR_INVALID_ARG;
+  if (a->K % mla::kCkv != 0) return MLA_ERR_UNSUPPORTED;
+  // tokens and rows are 32-bit, and a grid dimension holds the token blocks
+  if ((int64_t)a->B * a->Q > 65535 * 8 || (int64_t)a->G * a->N > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+
+}  // namespace
+
+extern "C" size_t mla_fp4_linear_workspace_size(const mla_fp4_linear_args* a) {
+  return validate_fp4_linear(a) != MLA_OK ? 0 : mla::fp4_linear_workspace_bytes(a, sm_count());
+}
+
+extern "C" mla_status_t mla_fp4_linear(const mla_fp4_linear_args* a, void* workspace, size_t workspace_bytes,
+                                       void* stream) {
+  mla_status_t s = validate_fp4_linear(a);
+  if (s != MLA_OK) return s;
+  const size_t need = mla::fp4_linear_workspace_bytes(a, sm_count());
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return MLA_ERR_WORKSPACE;
+  return cuda_status(mla::launch_fp4_linear(a, workspace, sm_count(), (cudaStream_t)stream));
 }

@@ -20,6 +20,15 @@ Calls (same names as the C ABI):
 - ``mla_cache_append(c_kv, k_pe, kv_cache, pe_cache, seq_lens, ...)``: the
   step before the decode, writing the new tokens' rows (or FP4 entries) into
   the cache.
+- ``mla_rope_append(c_kv, k_pe, kv_cache, pe_cache, seq_lens, q_pe=...)``: the
+  same on raw projection outputs, rotating the rope rows and the queries'
+  position parts at their positions; one call takes prompts of any lengths.
+- ``mla_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache,
+  softmax_scale, ...)``: the decode of a batch whose sequences share a prefix
+  stored once; ``mla_prefix_decode_step`` is the whole step around it.
+- ``mla_fp4_linear(x, w, scale)``: products with weights held as FP4 entries
+  (``pack_fp4_weight`` makes them); ``mla_fp4_group_wo`` is ``mla_group_wo`` on
+  such weights.
 """
 from __future__ import annotations
 
@@ -57,6 +66,12 @@ _SIGS = {
     "mla_cache_append": (_c.c_int, [_c.c_void_p, _c.c_void_p]),
     "mla_group_wo_workspace_size": (_c.c_size_t, [_c.c_void_p]),
     "mla_group_wo": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "mla_rope_append": (_c.c_int, [_c.c_void_p, _c.c_void_p]),
+    "mla_prefix_decode_num_splits": (_c.c_int, [_c.c_void_p]),
+    "mla_prefix_decode_workspace_size": (_c.c_size_t, [_c.c_void_p]),
+    "mla_prefix_decode": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "mla_fp4_linear_workspace_size": (_c.c_size_t, [_c.c_void_p]),
+    "mla_fp4_linear": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
 }
 
 
@@ -107,6 +122,58 @@ class GroupWoArgs(ctypes.Structure):
         ("G", _c.c_int), ("R", _c.c_int), ("D", _c.c_int), ("dtype", _c.c_int),
         ("x", _c.c_void_p), ("wo_a", _c.c_void_p), ("wo_b", _c.c_void_p), ("out", _c.c_void_p),
         ("err_flag", _c.c_void_p),
+    ]
+
+
+class RopeAppendArgs(ctypes.Structure):
+    """Mirror of ``mla_rope_append_args`` in include/mla.h (field order and types)."""
+
+    _fields_ = [
+        ("B", _c.c_int), ("Q", _c.c_int), ("N", _c.c_int), ("Ckv", _c.c_int), ("Dr", _c.c_int),
+        ("H", _c.c_int), ("dtype", _c.c_int),
+        ("c_kv", _c.c_void_p), ("k_pe", _c.c_void_p), ("q_pe", _c.c_void_p), ("q_out", _c.c_void_p),
+        ("c_kv_stride", _c.c_int64), ("k_pe_stride", _c.c_int64),
+        ("q_token_stride", _c.c_int64), ("q_head_stride", _c.c_int64),
+        ("o_batch_stride", _c.c_int64), ("o_token_stride", _c.c_int64), ("o_head_stride", _c.c_int64),
+        ("kv_cache", _c.c_void_p), ("pe_cache", _c.c_void_p),
+        ("kv_row_stride", _c.c_int64), ("pe_row_stride", _c.c_int64),
+        ("kv_batch_stride", _c.c_int64), ("pe_batch_stride", _c.c_int64),
+        ("Lk", _c.c_int), ("seq_lens", _c.c_void_p), ("block_table", _c.c_void_p),
+        ("max_pages", _c.c_int), ("page_size", _c.c_int), ("num_pages", _c.c_int),
+        ("cu_tokens", _c.c_void_p), ("pos_offset", _c.c_int), ("rope_theta", _c.c_float),
+        ("err_flag", _c.c_void_p),
+    ]
+
+
+class PrefixArgs(ctypes.Structure):
+    """Mirror of ``mla_prefix_args`` in include/mla.h (field order and types)."""
+
+    _fields_ = [
+        ("B", _c.c_int), ("H", _c.c_int), ("Q", _c.c_int), ("Ckv", _c.c_int), ("Dr", _c.c_int),
+        ("dtype", _c.c_int), ("q_lat", _c.c_void_p), ("q_pe", _c.c_void_p),
+        ("prefix_kv", _c.c_void_p), ("prefix_pe", _c.c_void_p),
+        ("prefix_kv_stride", _c.c_int64), ("prefix_pe_stride", _c.c_int64), ("prefix_len", _c.c_int),
+        ("prefix_table", _c.c_void_p), ("prefix_num_pages", _c.c_int),
+        ("kv_cache", _c.c_void_p), ("pe_cache", _c.c_void_p),
+        ("kv_row_stride", _c.c_int64), ("pe_row_stride", _c.c_int64),
+        ("kv_batch_stride", _c.c_int64), ("pe_batch_stride", _c.c_int64),
+        ("Lk", _c.c_int), ("seq_lens", _c.c_void_p), ("block_table", _c.c_void_p),
+        ("max_pages", _c.c_int), ("page_size", _c.c_int), ("num_pages", _c.c_int),
+        ("causal_mask", _c.c_void_p), ("causal", _c.c_int), ("softmax_scale", _c.c_float),
+        ("sinks", _c.c_void_p), ("num_splits", _c.c_int), ("x", _c.c_void_p), ("lse", _c.c_void_p),
+        ("err_flag", _c.c_void_p),
+    ]
+
+
+class Fp4LinearArgs(ctypes.Structure):
+    """Mirror of ``mla_fp4_linear_args`` in include/mla.h (field order and types)."""
+
+    _fields_ = [
+        ("B", _c.c_int), ("Q", _c.c_int), ("G", _c.c_int), ("N", _c.c_int), ("K", _c.c_int),
+        ("x", _c.c_void_p),
+        ("x_batch_stride", _c.c_int64), ("x_token_stride", _c.c_int64),
+        ("x_group_stride", _c.c_int64), ("x_block_stride", _c.c_int64),
+        ("w", _c.c_void_p), ("scale", _c.c_float), ("out", _c.c_void_p),
     ]
 
 
@@ -423,3 +490,375 @@ def launch_group_wo(call: GroupWoCall, stream=None) -> torch.Tensor:
 def mla_group_wo(x, wo_a, wo_b=None, *, stream=None, **kw) -> torch.Tensor:
     """Grouped low-rank output projection after the inverse RoPE -> (B,Q,D) or (B,Q,G*R)."""
     return launch_group_wo(make_group_wo(x, wo_a, wo_b, **kw), stream=stream)
+
+
+# --- the step on raw projection outputs, shared prefixes and FP4 weights -----
+
+def _need(cond: bool, what: str) -> None:
+    if not cond:
+        raise MlaError(what)
+
+
+def _int32(t, name: str, n: Optional[int] = None) -> None:
+    """``t`` (None allowed) is a contiguous int32 tensor, of ``n`` elements when given."""
+    if t is not None:
+        _need(t.dtype == torch.int32 and t.is_contiguous(), f"{name} must be contiguous int32")
+        _need(n is None or t.numel() == n, f"{name} must have {n} elements")
+
+
+def _one_device(first: torch.Tensor, *ts) -> None:
+    _need_cuda(first, *ts)
+    for t in ts:
+        _need(t is None or t.device == first.device, "tensors are on different devices")
+
+
+class _on:
+    """The device and stream of a call: ``t``'s device is current inside, and
+    ``.stream`` is ``stream`` or that device's current stream. Memory allocated
+    for the call is tied to that stream with :meth:`used`."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        self.device, self.given = t.device, stream
+
+    def __enter__(self):
+        self._guard = torch.cuda.device(self.device)
+        self._guard.__enter__()
+        current = torch.cuda.current_stream(self.device)
+        self.stream = _stream(current if self.given is None else self.given)
+        self._other = self.stream != current.cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        return self._guard.__exit__(*exc)
+
+    def used(self, *ts) -> None:
+        if self._other:
+            s = torch.cuda.ExternalStream(self.stream, device=self.device)
+            for t in ts:
+                if t is not None:
+                    t.record_stream(s)
+
+
+def _cache_fields(a, kv_cache, pe_cache, block_table, page_size: int, Lk: Optional[int], B: int) -> None:
+    """Fill the cache part of an argument struct: (B, Lk, C) views, or
+    (num_pages, page_size, C) pools with a (B, max_pages) ``block_table``."""
+    for t in (kv_cache, pe_cache):
+        _need(t is None or (t.dim() == 3 and t.stride(-1) == 1), "cache tensors are 3-D with a packed last dim")
+    a.kv_cache, a.pe_cache = _ptr(kv_cache), _ptr(pe_cache)
+    a.kv_row_stride, a.kv_batch_stride = kv_cache.stride(1), kv_cache.stride(0)
+    if pe_cache is not None:
+        _need(pe_cache.shape[:2] == kv_cache.shape[:2], "kv_cache and pe_cache hold different rows")
+        a.pe_row_stride, a.pe_batch_stride = pe_cache.stride(1), pe_cache.stride(0)
+    if block_table is not None:
+        _int32(block_table, "block_table")
+        _need(block_table.dim() == 2 and block_table.shape[0] == B, "block_table must be (B, max_pages)")
+        _need(kv_cache.shape[1] == page_size, "the pool's pages must have page_size rows")
+        for t in (kv_cache, pe_cache):
+            _need(t is None or t.shape[0] == 1 or t.stride(0) == page_size * t.stride(1),
+                  "a pool's pages must follow each other")
+        a.block_table = _ptr(block_table)
+        a.max_pages, a.page_size, a.num_pages = block_table.shape[1], page_size, kv_cache.shape[0]
+        a.kv_batch_stride = a.pe_batch_stride = 0
+        a.Lk = Lk if Lk is not None else a.max_pages * page_size
+    else:
+        _need(kv_cache.shape[0] == B, "a contiguous cache must be (B, Lk, C)")
+        a.Lk = Lk if Lk is not None else kv_cache.shape[1]
+        _need(a.Lk <= kv_cache.shape[1], "Lk is beyond the cache's rows")
+
+
+def make_rope_append_args(c_kv, k_pe, kv_cache, pe_cache, seq_lens, *, q_pe=None, q_out=None, cu_tokens=None,
+                          block_table=None, page_size: int = 64, pos_offset: int = 0,
+                          rope_theta: float = 10000.0, err_flag=None, Lk: Optional[int] = None):
+    """Fill a RopeAppendArgs from tensors (no GPU work); returns (args, q_out).
+
+    Without ``cu_tokens``: c_kv (B, Q, 512), k_pe (B, Q, Dr), q_pe (B, Q, H, Dr),
+    q_out (B, H, Q, Dr). With ``cu_tokens`` (B+1) int32: c_kv (N, 512), k_pe
+    (N, Dr), q_pe and q_out (N, H, Dr). Any strides with a packed last dim
+    (slices of wider projection rows); the tokens of c_kv, k_pe and q_pe must
+    step evenly.
+    """
+    _one_device(c_kv, k_pe, kv_cache, pe_cache, seq_lens, q_pe, q_out, cu_tokens, block_table, err_flag)
+    _need(all(t.dtype == c_kv.dtype for t in (k_pe, kv_cache, pe_cache, q_pe, q_out) if t is not None),
+          "mla_rope_append: tensors must share one dtype")
+    B = seq_lens.numel()
+    _int32(seq_lens, "seq_lens")
+    _int32(cu_tokens, "cu_tokens", B + 1)
+    _int32(err_flag, "err_flag")
+    a = RopeAppendArgs()
+    lead = 1 if cu_tokens is not None else 2
+    _need(c_kv.dim() == lead + 1 and k_pe.dim() == lead + 1 and k_pe.shape[:-1] == c_kv.shape[:-1],
+          "mla_rope_append: c_kv and k_pe must hold the same tokens")
+    _need(lead == 1 or c_kv.shape[0] == B, "mla_rope_append: c_kv must be (B, Q, 512)")
+    a.B, a.Ckv, a.Dr, a.dtype = B, c_kv.shape[-1], k_pe.shape[-1], _qdtype(c_kv)
+    a.N = c_kv.shape[:-1].numel()
+    a.Q = c_kv.shape[1] if lead == 2 else 0
+
+    def token_stride(t: torch.Tensor) -> int:
+        _need(t.stride(-1) == 1, "mla_rope_append: the last dim must be packed")
+        if lead == 1:
+            return t.stride(0)
+        s = t.stride(1) if t.shape[1] > 1 else t.stride(0)
+        _need(t.shape[0] == 1 or t.shape[1] == 1 or t.stride(0) == t.shape[1] * s,
+              "mla_rope_append: tokens must step evenly")
+        return s
+
+    a.c_kv, a.k_pe = _ptr(c_kv), _ptr(k_pe)
+    a.c_kv_stride, a.k_pe_stride = token_stride(c_kv), token_stride(k_pe)
+    if q_pe is not None:
+        _need(q_pe.dim() == lead + 2 and q_pe.shape[:lead] == c_kv.shape[:-1] and q_pe.shape[-1] == a.Dr,
+              "mla_rope_append: q_pe must hold the tokens' heads, Dr wide")
+        a.H = q_pe.shape[-2]
+        shape = tuple(q_pe.shape) if lead == 1 else (B, a.H, a.Q, a.Dr)
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=q_pe.dtype, device=q_pe.device)
+        _need(tuple(q_out.shape) == shape and q_out.stride(-1) == 1, f"mla_rope_append: q_out must be {shape}")
+        a.q_pe, a.q_out = _ptr(q_pe), _ptr(q_out)
+        a.q_token_stride, a.q_head_stride = token_stride(q_pe), q_pe.stride(-2)
+        if lead == 1:
+            a.o_token_stride, a.o_head_stride = q_out.stride(0), q_out.stride(1)
+        else:
+            a.o_batch_stride, a.o_head_stride, a.o_token_stride = q_out.stride()[:3]
+    else:
+        _need(q_out is None, "mla_rope_append: q_out without q_pe")
+    _cache_fields(a, kv_cache, pe_cache, block_table, page_size, Lk, B)
+    _need(kv_cache.shape[-1] >= a.Ckv and pe_cache.shape[-1] >= a.Dr, "mla_rope_append: cache rows are too narrow")
+    a.seq_lens, a.cu_tokens, a.err_flag = _ptr(seq_lens), _ptr(cu_tokens), _ptr(err_flag)
+    a.pos_offset, a.rope_theta = int(pos_offset), float(rope_theta)
+    return a, q_out
+
+
+def mla_rope_append(c_kv, k_pe, kv_cache, pe_cache, seq_lens, *, stream=None, **kw) -> Optional[torch.Tensor]:
+    """Enqueue mla_rope_append: latent rows and rotated rope rows into the cache,
+    in place; returns the rotated queries (None without ``q_pe``).
+
+    Arguments as in :func:`make_rope_append_args`; ``seq_lens`` are the lengths
+    after the append. A token whose position or page is out of range is not
+    stored and sets DEVICE_ERR_BLOCK_TABLE in ``err_flag``.
+    """
+    a, q_out = make_rope_append_args(c_kv, k_pe, kv_cache, pe_cache, seq_lens, **kw)
+    with _on(c_kv, stream) as on:
+        _check(lib().mla_rope_append(ctypes.byref(a), on.stream), "mla_rope_append")
+        on.used(q_out)
+    return q_out
+
+
+@dataclass
+class PrefixCall:
+    """One mla_prefix_decode call: its arguments, workspace and outputs (build once, launch many times)."""
+
+    args: PrefixArgs
+    num_splits: int
+    workspace: Optional[torch.Tensor]
+    x: torch.Tensor
+    lse: Optional[torch.Tensor]
+    keep: list = field(default_factory=list)   # tensors the pointers in args refer to
+
+
+def make_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, softmax_scale: float, *,
+                       prefix_len: Optional[int] = None, prefix_table=None, seq_lens=None, block_table=None,
+                       page_size: int = 64, causal_mask=None, causal: bool = False, sinks=None,
+                       num_splits: int = 0, x=None, lse=None, want_lse: bool = True, workspace=None,
+                       err_flag=None, Lk: Optional[int] = None) -> PrefixCall:
+    """Prepare mla_prefix_decode (no GPU work): allocates x, lse and the workspace when not given.
+
+    prefix_kv / prefix_pe: (prefix_len, C) rows, or (pages, page_size, C) pools
+    with ``prefix_table`` and ``prefix_len``; None with ``prefix_len`` 0.
+    kv_cache / pe_cache: the sequences' own tokens, laid out as for mla_decode,
+    or None (no own tokens). ``causal_mask`` covers prefix_len + Lk positions.
+    """
+    _one_device(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, prefix_table, seq_lens, block_table,
+                causal_mask, sinks, x, lse, workspace, err_flag)
+    _need(q_lat.dim() == 4 and q_lat.is_contiguous(), "q_lat must be contiguous (B, H, Q, 512)")
+    B, H, Q, Ckv = q_lat.shape
+    _need(q_pe is None or (q_pe.is_contiguous() and q_pe.shape[:3] == q_lat.shape[:3]),
+          "q_pe must be contiguous (B, H, Q, Dr)")
+    a = PrefixArgs()
+    a.B, a.H, a.Q, a.Ckv = B, H, Q, Ckv
+    a.Dr = 0 if q_pe is None else q_pe.shape[-1]
+    a.dtype = _qdtype(q_lat)
+    for t in (q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, x):
+        _need(t is None or t.dtype == q_lat.dtype, "mla_prefix_decode: tensors must share one dtype")
+    a.q_lat, a.q_pe = _ptr(q_lat), _ptr(q_pe)
+    for t, w in ((prefix_kv, Ckv), (prefix_pe, a.Dr), (kv_cache, Ckv), (pe_cache, a.Dr)):
+        _need(t is None or t.shape[-1] >= w, "mla_prefix_decode: cache rows are too narrow")
+    _int32(prefix_table, "prefix_table")
+    if prefix_kv is not None:
+        dim = 2 if prefix_table is None else 3
+        _need(prefix_kv.dim() == dim and prefix_kv.stride(-1) == 1, f"prefix_kv must be {dim}-D, last dim packed")
+        a.prefix_kv, a.prefix_kv_stride = _ptr(prefix_kv), prefix_kv.stride(-2)
+        if a.Dr:
+            _need(prefix_pe is not None and prefix_pe.stride(-1) == 1 and prefix_pe.shape[:-1] == prefix_kv.shape[:-1],
+                  "prefix_pe must hold prefix_kv's rows")
+            a.prefix_pe, a.prefix_pe_stride = _ptr(prefix_pe), prefix_pe.stride(-2)
+        if prefix_table is None:
+            a.prefix_len = prefix_kv.shape[0] if prefix_len is None else prefix_len
+            _need(a.prefix_len <= prefix_kv.shape[0], "prefix_len is beyond prefix_kv's rows")
+        else:
+            _need(prefix_len is not None, "a paged prefix needs prefix_len")
+            _need(prefix_kv.shape[1] == page_size and prefix_table.numel() * page_size >= prefix_len,
+                  "prefix_table or page_size does not cover prefix_len")
+            for t in (prefix_kv, prefix_pe):
+                _need(t is None or t.shape[0] == 1 or t.stride(0) == page_size * t.stride(1),
+                      "a pool's pages must follow each other")
+            a.prefix_len, a.prefix_table, a.prefix_num_pages = prefix_len, _ptr(prefix_table), prefix_kv.shape[0]
+    else:
+        _need(not prefix_len, "prefix_len without prefix_kv")
+    a.page_size = page_size
+    if kv_cache is not None:
+        _need(a.Dr == 0 or pe_cache is not None, "pe_cache is missing")
+        _cache_fields(a, kv_cache, pe_cache if a.Dr else None, block_table, page_size, Lk, B)
+    else:
+        _need(not Lk, "Lk without kv_cache")
+    _int32(seq_lens, "seq_lens", B)
+    _int32(err_flag, "err_flag")
+    a.seq_lens = _ptr(seq_lens)
+    if causal_mask is not None:
+        causal_mask = causal_mask.reshape(-1).to(torch.uint8).contiguous()
+        _need(causal_mask.numel() >= a.prefix_len + a.Lk, "causal_mask must cover prefix_len + Lk positions")
+        a.causal_mask = _ptr(causal_mask)
+    a.causal, a.softmax_scale, a.num_splits = int(bool(causal)), float(softmax_scale), int(num_splits)
+    if sinks is not None:
+        _need(sinks.dtype == torch.float32 and sinks.is_contiguous() and sinks.numel() == H, "sinks must be (H) float32")
+        a.sinks = _ptr(sinks)
+    if x is None:
+        x = torch.empty((B, H, Q, Ckv), dtype=q_lat.dtype, device=q_lat.device)
+    _need(x.is_contiguous() and x.shape == q_lat.shape, "x must be contiguous (B, H, Q, 512)")
+    if lse is None and want_lse:
+        lse = torch.empty((B, H, Q), dtype=torch.float32, device=q_lat.device)
+    _need(lse is None or (lse.is_contiguous() and lse.dtype == torch.float32 and lse.numel() == B * H * Q),
+          "lse must be contiguous float32 (B, H, Q)")
+    a.x, a.lse, a.err_flag = _ptr(x), _ptr(lse), _ptr(err_flag)
+    with torch.cuda.device(q_lat.device):
+        S = lib().mla_prefix_decode_num_splits(ctypes.byref(a))
+        if S < 0:
+            raise MlaError("mla_prefix_decode arguments rejected (MLA_ERR_INVALID_ARG or MLA_ERR_UNSUPPORTED)")
+        need = int(lib().mla_prefix_decode_workspace_size(ctypes.byref(a)))
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q_lat.device)
+    _need(not need or workspace.numel() * workspace.element_size() >= need, "workspace is too small")
+    keep = [q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, prefix_table, seq_lens, block_table, causal_mask,
+            sinks, err_flag]
+    return PrefixCall(args=a, num_splits=S, workspace=workspace if need else None, x=x, lse=lse, keep=keep)
+
+
+def launch_prefix_decode(call: PrefixCall, stream=None):
+    """Enqueue a prepared call; returns its (x, lse)."""
+    ws = call.workspace
+    with _on(call.x, stream) as on:
+        _check(lib().mla_prefix_decode(ctypes.byref(call.args), _ptr(ws),
+                                       0 if ws is None else ws.numel() * ws.element_size(), on.stream),
+               "mla_prefix_decode")
+        on.used(call.x, call.lse, ws, *call.keep)
+    return call.x, call.lse
+
+
+def mla_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, softmax_scale: float, *,
+                      stream=None, **kw):
+    """Decode of a batch that shares a prefix; returns (x, lse), final when the enqueued work completes.
+
+    Arguments as in :func:`make_prefix_decode`. The call merges its split
+    partials itself: there is no combine to call after it.
+    """
+    return launch_prefix_decode(make_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache,
+                                                   softmax_scale, **kw), stream=stream)
+
+
+def mla_prefix_decode_step(q_nope, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, wkv_b, softmax_scale,
+                           causal_mask=None, **kw):
+    """mla_decode_step behind a shared prefix -> out (B,H,Q,Vd): absorb, prefix decode, up-project."""
+    Dn, stream = q_nope.shape[-1], kw.get("stream")
+    with torch.cuda.device(q_nope.device):
+        q_lat = mla_absorb_q(q_nope, wkv_b, stream=stream)
+        x, _ = mla_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, softmax_scale,
+                                 causal_mask=causal_mask, **kw)
+        out = mla_up_proj(x, wkv_b, Dn, stream=stream)
+    with _on(x, stream) as on:
+        on.used(q_lat, x, out)
+    return out
+
+
+FP4_BLOCK, FP4_ENTRY_BYTES = 512, 288
+
+
+def pack_fp4_weight(w: torch.Tensor, scale: Optional[float] = None, *, stream=None):
+    """Weights (..., N, K) as FP4 entries: returns (entries (..., N, K/512, 288) uint8, scale).
+
+    ``w / scale`` is quantised by mla_cache_append's FP4 rule (an E4M3 scale per
+    16 channels, E2M1 codes), so W ~ scale * value. Without ``scale`` it is chosen
+    so that the largest weight meets the format's end (448 * 6); that reads the
+    maximum back to the host. Done once, when weights are loaded.
+    """
+    _need_cuda(w)
+    _need(w.dim() >= 2 and w.shape[-1] % FP4_BLOCK == 0, "pack_fp4_weight: K must be a multiple of 512")
+    wf = w.float()
+    if scale is None:
+        scale = float(wf.abs().max()) / (448.0 * 6.0) or 1.0
+    rows = (wf / scale).reshape(1, -1, FP4_BLOCK).contiguous()
+    n = rows.shape[1]
+    _need(n < 2 ** 31, "pack_fp4_weight: too many entries")
+    entries = torch.empty((1, n, FP4_ENTRY_BYTES), dtype=torch.uint8, device=w.device)
+    lens = torch.full((1,), n, dtype=torch.int32, device=w.device)
+    with _on(w, stream) as on:
+        mla_cache_append(rows, None, entries, None, lens, stream=on.stream)
+        on.used(rows, entries, lens)
+    return entries.reshape(*w.shape[:-1], w.shape[-1] // FP4_BLOCK, FP4_ENTRY_BYTES), scale
+
+
+def _fp4_linear(x, a: Fp4LinearArgs, w, scale: float, out, stream):
+    """Check what both callers share, allocate, launch."""
+    _one_device(x, w, out)
+    _need(x.dtype == torch.bfloat16, "mla_fp4_linear takes bf16 activations")
+    _need(w.dtype == torch.uint8 and w.is_contiguous() and w.shape[-1] == FP4_ENTRY_BYTES,
+          "mla_fp4_linear weights are contiguous uint8 entries of 288 bytes")
+    _need(out.dtype == torch.bfloat16 and out.is_contiguous(), "mla_fp4_linear: out must be contiguous bf16")
+    a.x, a.w, a.out, a.scale = _ptr(x), _ptr(w), _ptr(out), float(scale)
+    if x.numel() == 0:
+        return out
+    with _on(x, stream) as on:
+        need = int(lib().mla_fp4_linear_workspace_size(ctypes.byref(a)))
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        _check(lib().mla_fp4_linear(ctypes.byref(a), _ptr(ws), need, on.stream), "mla_fp4_linear")
+        on.used(ws, out)
+    return out
+
+
+def mla_fp4_linear(x: torch.Tensor, w: torch.Tensor, scale: float = 1.0, *, out: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """out[..., n] = scale * sum_k x[..., k] W[n, k]: x (..., K) bf16, w (N, K/512, 288) FP4 entries."""
+    _need(w.dim() == 3 and x.dim() >= 1 and x.shape[-1] == w.shape[1] * FP4_BLOCK,
+          "mla_fp4_linear: w must be (N, K/512, 288) for x (..., K)")
+    N, K = w.shape[0], x.shape[-1]
+    x2 = x.reshape(-1, K)
+    if x2.stride(-1) != 1 or x2.stride(0) % 8 or x2.data_ptr() % 16:
+        x2 = x2.contiguous()
+    if out is None:
+        out = torch.empty((*x.shape[:-1], N), dtype=torch.bfloat16, device=x.device)
+    _need(tuple(out.shape) == (*x.shape[:-1], N), "mla_fp4_linear: out has another shape")
+    a = Fp4LinearArgs()
+    a.B, a.Q, a.G, a.N, a.K = x2.shape[0], 1, 1, N, K
+    a.x_batch_stride, a.x_block_stride = x2.stride(0), FP4_BLOCK
+    return _fp4_linear(x2, a, w, scale, out, stream)
+
+
+def mla_fp4_group_wo(x: torch.Tensor, wo_a: torch.Tensor, wo_b: Optional[torch.Tensor] = None, *,
+                     scale_a: float = 1.0, scale_b: float = 1.0, out: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """mla_group_wo on FP4 weights -> (B,Q,D), or (B,Q,G*R) without ``wo_b``.
+
+    x (B,H,Q,512) bf16; wo_a (G,R,H/G,288) entries of (G, R, (H/G)*512) weights;
+    wo_b (D,G*R/512,288). z is rounded to bf16 between the factors, as there.
+    """
+    _need(x.dim() == 4 and x.shape[-1] == FP4_BLOCK and x.stride(-1) == 1, "mla_fp4_group_wo: x must be (B, H, Q, 512)")
+    B, H, Q, _ = x.shape
+    _need(wo_a.dim() == 4 and wo_a.shape[0] * wo_a.shape[2] == H, "mla_fp4_group_wo: wo_a must be (G, R, H/G, 288)")
+    G, R, per, _ = wo_a.shape
+    if x.data_ptr() % 16 or any(s % 8 for s in x.stride()[:3]):
+        x = x.contiguous()
+    z = out if wo_b is None and out is not None else torch.empty((B, Q, G * R), dtype=torch.bfloat16, device=x.device)
+    _need(tuple(z.shape) == (B, Q, G * R), "mla_fp4_group_wo: out has another shape")
+    a = Fp4LinearArgs()
+    a.B, a.Q, a.G, a.N, a.K = B, Q, G, R, per * FP4_BLOCK
+    a.x_batch_stride, a.x_block_stride, a.x_token_stride = x.stride()[:3]
+    a.x_group_stride = per * x.stride(1)
+    _fp4_linear(x, a, wo_a, scale_a, z, stream)
+    return z if wo_b is None else mla_fp4_linear(z, wo_b, scale_b, out=out, stream=stream)
