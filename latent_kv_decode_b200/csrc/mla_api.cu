@@ -500,7 +500,8 @@ mla_status_t validate_prefix(const mla_prefix_args* a) {
 
 int prefix_splits(const mla_prefix_args* a) {
   if (a->num_splits > 0) return a->num_splits;
-  return mla::prefix_simt_auto_splits(a, sm_count());
+  return mla::prefix_sm100_supported(a) ? mla::prefix_sm100_auto_splits(a, sm_count())
+                                        : mla::prefix_simt_auto_splits(a, sm_count());
 }
 
 size_t prefix_ws_o_bytes(const mla_prefix_args* a, int S) {
@@ -573,7 +574,7 @@ extern "C" mla_status_t mla_prefix_decode(const mla_prefix_args* a, void* worksp
   }
   cudaStream_t st = (cudaStream_t)stream;
   const bool bf16 = a->dtype == MLA_BF16;
-  s = cuda_status(mla::launch_prefix_simt(p, bf16, st));
+  s = cuda_status(mla::prefix_sm100_supported(a) ? mla::launch_prefix_sm100(p, st) : mla::launch_prefix_simt(p, bf16, st));
   if (s != MLA_OK || S == 1) return s;
   return cuda_status(mla::launch_prefix_combine(p, bf16, st));
 }

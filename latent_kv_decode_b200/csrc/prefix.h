@@ -101,6 +101,10 @@ size_t prefix_simt_smem(int D);
 cudaError_t launch_prefix_simt(const PrefixParams& p, bool bf16, cudaStream_t st);
 int prefix_simt_auto_splits(const mla_prefix_args* a, int sms);
 
+bool prefix_sm100_supported(const mla_prefix_args* a);
+int prefix_sm100_auto_splits(const mla_prefix_args* a, int sms);
+cudaError_t launch_prefix_sm100(const PrefixParams& p, cudaStream_t st);
+
 // merges the split partials in p.ws_o / p.ws_lse into p.x / p.lse
 cudaError_t launch_prefix_combine(const PrefixParams& p, bool bf16, cudaStream_t st);
 

@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(256) prefix_simt(const PrefixParams p) {
         l = l * wt + expf(sk - m2);
         m = m2;
       }
-      const bool seen = m != -INFINITY;          // a NaN denominator stays one
+      const bool seen = !(m == -INFINITY && l == 0.f);   // a NaN denominator stays one
       inv = seen ? wt / l : 0.f;
       const float lse = seen ? m + logf(l) : -INFINITY;
       if (split)
