@@ -22,22 +22,22 @@
 //   O^T += V^T . P^T   pair MMA, M = 256 latent dims (CTA r: dims 256n + 128r ..
 //                      + 127 for n = 0, 1), N = the 128 rows, K = the tokens.
 //
-// Each CTA loads its own 64 tokens of a tile once (two 32 KB boxes: latent
-// chunks 0, 1, 4, 5 into slots 0-3 of the tile's set, 2, 3, 6, 7 into slots 4-7;
-// and the rope chunk), and, once S has used them, the other CTA's tokens of its
+// Each CTA loads its own 64 tokens of a tile once (four 16 KB boxes: latent
+// chunks 0-1, 4-5, 2-3, 6-7 into slots 0-1, 2-3, 4-5, 6-7 of the tile's set; and
+// the rope chunk), and, once S has used them, the other CTA's tokens of its
 // own dims over the four slots it does not aggregate. Tokens of CTA 0 are then
 // in slots 0-3 and tokens of CTA 1 in slots 4-7 of both CTAs.
 //
 // A weight of 0 does not silence an infinity or NaN in V. Tiles that may hold
 // rows which some query must not see ("guarded": own tokens, a tile's ragged
-// end, a mask, a bad page) are cleaned before the aggregation: warp 6 zeroes
+// end, a mask, a bad page) are cleaned before the aggregation: warp 2 zeroes
 // the rows no query may see, and if S shows a non-finite key, the softmax warps
 // zero the non-finite values (the rows that see that key are NaN by their S).
 //
 // Warps (384 threads): 0 own-token producer (+ Q), 1 QK issuer (CTA 0) and TMEM
-// owner, 2-5 and 8-11 softmax + epilogue (TMEM lane = 32 (warp % 4) + lane; the
-// two sets split a lane's 64 scores), 6 peer-token producer and cleaner, 7 PV
-// issuer (CTA 0). Every wait is bounded; a timeout sets MLA_DEVICE_ERR_TIMEOUT
+// owner, 2 peer-token producer and cleaner, 3 PV issuer (CTA 0), 4-11 softmax +
+// epilogue (TMEM lane = 32 (warp % 4) + lane; the two sets of four split a lane's
+// 64 scores). Every wait is bounded; a timeout sets MLA_DEVICE_ERR_TIMEOUT
 // and the kernel unwinds.
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -51,7 +51,10 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 384;
+constexpr int kSets = 2;                    // softmax warp sets; each reads 64 / kSets tokens of a lane
+constexpr int kSoft = 128 * kSets;          // softmax threads (warps 4 and up)
+constexpr int kSoftWarps = kSoft / 32;
+constexpr int kThreads = 128 + kSoft;
 constexpr int kTileT = 128;                 // tokens per tile (both CTAs)
 constexpr int kRowsT = 128;                 // stacked rows per cluster
 constexpr int kChunk = 8192;                // 64 rows (tokens or query rows) x 128 B
@@ -63,32 +66,30 @@ constexpr int kOffP = kOffR + kChunk;       // P: 2 blocks (tokens 0-63, 64-127)
 constexpr int kBigBytes = kOffP + 2 * kChunk;   // the 1024-aligned operand region
 enum : int {
   B_QFULL = 0,
-  B_KF0 = 1,              // [2] slots 0-3 of both CTAs landed
-  B_KF1 = 3,              // [2] slots 4-7 of both CTAs landed
-  B_XF = 5,               // [2] peer-token boxes landed (of both CTAs; a guarded tile: of CTA 0)
-  B_SFULL = 7,            // [2] S(j) computed (both CTAs, multicast commit)
-  B_PFULL = 9,            // [2] P(j) written, O^T rescaled, V clean in both CTAs (count 2)
-  B_PVDONE = 11,          // [2] O^T += V^T P^T of tile j done (both CTAs, multicast)
-  B_QH0 = 13,             // [2] QK(j) over slots 0-3 done (both CTAs, multicast)
-  B_PVX = 15,             // [2] PV(j) over slots 0-3 done (both CTAs, multicast)
-  B_AX = 17,              // [2] the peer's eight warps' flags of tile j arrived
-  B_RF = 19,              // the rope chunk of tile j of both CTAs landed (phase j)
-  B_RFREE = 20,           // QK(j) over the rope chunk done: the rope slot is free (multicast)
-  B_AL = 21,              // the peer's 64 rescale factors arrived (phase: moves so far)
-  B_EPX = 22,             // the peer's output scales arrived
-  B_XL = 23,              // CTA 1: its peer-token box of a guarded tile landed
-  B_ZD = 24,              // [2] this CTA's rows of a guarded tile are clean (phase: guarded tiles so far)
-  B_COUNT = 26
+  B_KF = 1,               // [2][4] slots 2i, 2i+1 of both CTAs landed
+  B_PV = 9,               // [2][4] PV(j) over slots 2i, 2i+1 (and before) done (both CTAs, multicast)
+  B_XF = 17,              // [2] peer-token boxes landed (of both CTAs; a guarded tile: of CTA 0)
+  B_SFULL = 19,           // [2] S(j) computed (both CTAs, multicast commit)
+  B_PFULL = 21,           // [2] P(j) written, O^T rescaled, V clean in both CTAs (count 2)
+  B_QH0 = 23,             // [2] QK(j) over slots 0-3 done (both CTAs, multicast)
+  B_AX = 25,              // [2] the flags of the peer's softmax warps for tile j arrived
+  B_RF = 27,              // the rope chunk of tile j of both CTAs landed (phase j)
+  B_RFREE = 28,           // QK(j) over the rope chunk done: the rope slot is free (multicast)
+  B_AL = 29,              // the peer's 64 rescale factors arrived (phase: moves so far)
+  B_EPX = 30,             // the peer's output scales arrived
+  B_XL = 31,              // CTA 1: its peer-token box of a guarded tile landed
+  B_ZD = 32,              // [2] this CTA's rows of a guarded tile are clean (phase: guarded tiles so far)
+  B_COUNT = 34
 };
 // Control block: barriers, TMEM address, abort flag, the peer's flags. In the
 // alignment gap below the operand region when it fits there, else after the
 // exchange block (row statistics, rescale factors, output scales).
 constexpr int kOffTmemPtr = 8 * B_COUNT;
 constexpr int kOffAbort = kOffTmemPtr + 4;
-constexpr int kOffFlags = (kOffAbort + 4 + 15) & ~15;     // int [4 tiles][8 warps of the peer]
-constexpr int kCtrlBytes = kOffFlags + 4 * 8 * 4;
-constexpr int kOffXmax = kBigBytes;                       // float [2 sets][128 lanes]
-constexpr int kOffAlpha = kOffXmax + 1024;                // float [128]
+constexpr int kOffFlags = (kOffAbort + 4 + 15) & ~15;     // int [2 tiles][16 warps of the peer]
+constexpr int kCtrlBytes = kOffFlags + 2 * kSoftWarps * 4;
+constexpr int kOffXmax = kBigBytes;                       // float [sets][128 lanes]
+constexpr int kOffAlpha = kOffXmax + 512 * kSets;                // float [128]
 constexpr int kOffScl = kOffAlpha + 512;                  // float [128]
 constexpr int kXchgEnd = kOffScl + 512;
 constexpr int kSmemAlloc = 232448;                        // the per-block limit
@@ -99,6 +100,8 @@ constexpr uint32_t kColS = 0;               // S buffers at columns 0 and 64 (pa
 constexpr uint32_t kColO = 128;             // O^T halves n = 0, 1 at columns 128 and 256
 constexpr uint32_t kTmemCols = 512;
 
+constexpr int kTok = 64 / kSets;            // scores of a tile per softmax thread
+constexpr uint32_t kAll = 0xffffffffu >> (32 - kTok);
 constexpr float kMove = 60.0f;              // log2: how far a score may exceed its row's reference
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -106,13 +109,47 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct alignas(64) TcParams {
   CUtensorMap tm_q;        // q_lat (N, 512), box 64 x 64
   CUtensorMap tm_qpe;      // q_pe (N, Dr), box 64 x 64 (columns beyond Dr read as 0)
-  CUtensorMap tm_kv[2];    // prefix, own: (64 dims, rows, 4 chunks, 2 groups of 4, seq | page),
-                           // box 64 rows x 2 chunks x 2 groups = chunks c, c+1, c+4, c+5
+  CUtensorMap tm_kv[2];    // prefix, own: (64 dims, rows, 8 chunks, seq | page), box 64 rows x 2 chunks
+  CUtensorMap tm_kx[2];    // the same as (64 dims, rows, 4 chunks, 2 groups of 4, seq | page), box
+                           // 64 rows x 2 chunks x 2 groups = chunks c, c+1, c+4, c+5
   CUtensorMap tm_pe[2];    // prefix, own: (Dr, rows, seq | page), box 64 x 64 rows
   PrefixParams p;
   float scale_log2;
   int blocks;              // 128-row blocks
 };
+
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(e));
+  return e;
+}
+
+// The pair MMA and its commit for a converged warp whose elected lane (e != 0)
+// issues them. The surrounding loop stays uniform, so descriptors live in
+// uniform registers: issued from a single-lane branch, an MMA took 50-60 ns of
+// register moves, twice what the tensor pipe needs for it.
+__device__ __forceinline__ void mma_pair(uint32_t e, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 z;\n\t"
+      "mov.b32 z, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {z, z, z, z, z, z, z, z}, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(e)
+      : "memory");
+}
+
+__device__ __forceinline__ void commit_pair(uint32_t e, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t.reg .b16 m;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "mov.b16 m, 3;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar),
+      "r"(e)
+      : "memory");
+}
 
 // 2^x on the SFU; subnormal results flush to zero (a weight below 2^-126 of the
 // row's reference, and so of its maximum).
@@ -183,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
   uint8_t* ctrl_p = smem_raw + (ctrl - raw);
   const PrefixParams& p = P.p;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp-uniform
   const uint32_t rank = cluster_ctarank();
   const int item = blockIdx.x >> 1;
   const int rb = item % P.blocks, z = item / P.blocks;   // clusters of one range run together
@@ -203,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(ctrl_p + kOffTmemPtr);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(ctrl_p + kOffTmemPtr), 0);
   // everything above overlaps the previous kernel; inputs are read from here on
   pdl_wait();
   const int r0 = rb * kRowsT;
@@ -211,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
   const int tiles = TileWalk<kTileT>::count(p, b0, b1);
   const int per = (tiles + p.num_splits - 1) / p.num_splits;
   const int j_begin = min(tiles, z * per);
-  const int ntiles = min(tiles, j_begin + per) - j_begin;
+  const int ntiles = __shfl_sync(0xffffffffu, min(tiles, j_begin + per) - j_begin, 0);
   TileWalk<kTileT> w;
   w.seek(p, b0, b1, j_begin);
   const bool rope = p.Dr > 0;
@@ -247,15 +284,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
           if (rank == 0) mbar_arrive_expect_tx(bar(B_RF), 2 * kChunk);
           tma_load_3d_2sm(sb0 + kOffR, &P.tm_pe[w.b < 0 ? 0 : 1], map_to_rank(bar(B_RF), 0), 0, k.y, k.zc);
         }
-        // slots 0-3 of set s held tile j-2 until the first half of its aggregation
-        if (j >= 2 && !mbar_wait_cluster(bar(B_PVX + s), ((j - 2) >> 1) & 1)) { ok = false; break; }
-        const uint32_t dst = sb0 + kOffL + s * 8 * kChunk;
-        if (rank == 0) mbar_arrive_expect_tx(bar(B_KF0 + s), 2 * 4 * kChunk);
-        tma_load_5d_2sm(dst, kv, map_to_rank(bar(B_KF0 + s), 0), 0, k.y, 0, 0, k.zc);
-        // slots 4-7 until the second half
-        if (j >= 2 && !mbar_wait_cluster(bar(B_PVDONE + s), ((j - 2) >> 1) & 1)) { ok = false; break; }
-        if (rank == 0) mbar_arrive_expect_tx(bar(B_KF1 + s), 2 * 4 * kChunk);
-        tma_load_5d_2sm(dst + 4 * kChunk, kv, map_to_rank(bar(B_KF1 + s), 0), 0, k.y, 2, 0, k.zc);
+        // slots 2i, 2i+1 of set s held tile j-2 until its aggregation passed them
+        for (int i = 0; i < 4; ++i) {
+          if (j >= 2 && !mbar_wait_cluster(bar(B_PV + 4 * s + i), ((j - 2) >> 1) & 1)) { ok = false; break; }
+          if (rank == 0) mbar_arrive_expect_tx(bar(B_KF + 4 * s + i), 2 * 2 * kChunk);
+          tma_load_4d_2sm(sb0 + kOffL + (s * 8 + 2 * i) * kChunk, kv, map_to_rank(bar(B_KF + 4 * s + i), 0), 0, k.y,
+                          ((i & 1) << 2) | (i & 2), k.zc);
+        }
         if (*abort_flag) ok = false;
         w.next(p, b0);
       }
@@ -265,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
       }
     }
     __syncwarp();
-  } else if (warp == 6) {
+  } else if (warp == 2) {
     // ------------------------------------------------------------------ peer-token producer, cleaner
     // The peer tokens' chunks of this CTA's dims (CTA 0: chunks 0, 1, 4, 5; CTA
     // 1: 2, 3, 6, 7) go, as one box, over the four slots of the chunks this CTA
@@ -285,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
           const bool local = g && rank == 1;
           if (rank == 0) mbar_arrive_expect_tx(bar(B_XF + s), (g ? 4 : 8) * kChunk);
           if (local) mbar_arrive_expect_tx(bar(B_XL), 4 * kChunk);
-          tma_load_5d_2sm(sb0 + kOffL + (s * 8 + 4 * (1 - (int)rank)) * kChunk, &P.tm_kv[w.b < 0 ? 0 : 1],
+          tma_load_5d_2sm(sb0 + kOffL + (s * 8 + 4 * (1 - (int)rank)) * kChunk, &P.tm_kx[w.b < 0 ? 0 : 1],
                           local ? map_to_rank(bar(B_XL), 1) : map_to_rank(bar(B_XF + s), 0), 0, peer.y,
                           2 * (int)rank, 0, peer.zc);
         }
@@ -328,89 +363,90 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ QK issuer (CTA 0)
-    // S(j) = Q . K^T in three groups as their data lands: the rope chunk (then a
-    // commit that frees its slot for tile j+1), slots 0-3 (then a commit that
-    // frees them for CTA 1's peer-token box), slots 4-7. The S buffer was read by
+    // S(j) = Q . K^T in five groups as their data lands: the rope chunk (then a
+    // commit that frees its slot for tile j+1), then two slots at a time (after
+    // slots 0-3 a commit that frees them for CTA 1's peer-token box). The S buffer was read by
     // softmax(j-2) once P(j-2) is complete.
-    if (rank == 0 && lane == 0 && ntiles > 0) {
+    if (rank == 0 && ntiles > 0) {
+      const uint32_t el = elect_one();
       const uint32_t idesc_qk = idesc_bf16_f32(128, 128, false, false);
       const uint64_t qd0 = smem_desc(sb0 + kOffQ, 16, 1024, kSwizzle128B);
       const uint64_t kd0 = smem_desc(sb0 + kOffL, 16, 1024, kSwizzle128B);
       const uint64_t rd0 = smem_desc(sb0 + kOffR, 16, 1024, kSwizzle128B);
-      bool ok = mbar_wait_cluster(bar(B_QFULL), 0);
+      bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar(B_QFULL), 0));
       for (int j = 0; j < ntiles && ok; ++j) {
         const int s = j & 1;
         const uint32_t d = tmem + kColS + 64u * s;
-        if (j >= 2) ok = mbar_wait_cluster(bar(B_PFULL + s), ((j - 2) >> 1) & 1);
-#pragma unroll 1
-        for (int g3 = rope ? 0 : 1; g3 < 3 && ok; ++g3) {
-          ok = g3 == 0 ? mbar_wait_cluster(bar(B_RF), j & 1)
-                       : mbar_wait_cluster(bar((g3 == 1 ? B_KF0 : B_KF1) + s), (j >> 1) & 1);
-          if (!ok) break;
+        if (j >= 2) ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar(B_PFULL + s), ((j - 2) >> 1) & 1));
+        if (rope && ok) {
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar(B_RF), j & 1));
           tc_fence_after();
-          const int nc = g3 == 0 ? 1 : 4;
-          const bool first = g3 == (rope ? 0 : 1);
-#pragma unroll 1
-          for (int cc = 0; cc < nc; ++cc) {
-            // the rope, then slot 4 (g3 - 1) + cc holding latent chunk (0, 1, 4, 5, 2, 3, 6, 7)[slot]
-            const int slot = 4 * (g3 - 1) + cc;
-            const int c = g3 == 0 ? 8 : ((slot & 2) << 1) | ((slot & 4) >> 1) | (slot & 1);
-            const uint64_t qd = desc_advance(qd0, c * kChunk);
-            const uint64_t kd = g3 == 0 ? rd0 : desc_advance(kd0, (s * 8 + slot) * kChunk);
+          const uint64_t qd = desc_advance(qd0, 8 * kChunk);
+          if (ok) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_bf16_ss_2sm(d, desc_advance(qd, 32 * k), desc_advance(kd, 32 * k), idesc_qk,
-                              !(first && cc == 0 && k == 0));
+              mma_pair(el, d, desc_advance(qd, 32 * k), desc_advance(rd0, 32 * k), idesc_qk, k != 0);
+            commit_pair(el, bar(B_RFREE));
           }
-          if (g3 == 0) mma_commit_2sm_mc(bar(B_RFREE), 3);
-          if (g3 == 1) mma_commit_2sm_mc(bar(B_QH0 + s), 3);
         }
-        if (ok) mma_commit_2sm_mc(bar(B_SFULL + s), 3);
-        if (*abort_flag) ok = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar(B_KF + 4 * s + i), (j >> 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            // slot 2i + cc holds latent chunk (0, 1, 4, 5, 2, 3, 6, 7)[slot]
+            const uint64_t qd = desc_advance(qd0, (((i & 1) << 2) | (i & 2) | cc) * kChunk);
+            const uint64_t kd = desc_advance(kd0, (s * 8 + 2 * i + cc) * kChunk);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_pair(el, d, desc_advance(qd, 32 * k), desc_advance(kd, 32 * k), idesc_qk,
+                       rope || i > 0 || cc > 0 || k > 0);
+          }
+          if (i == 1) commit_pair(el, bar(B_QH0 + s));
+        }
+        if (ok) commit_pair(el, bar(B_SFULL + s));
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) ok = false;
       }
-      if (!ok) fail();
+      if (!ok && lane == 0) fail();
     }
     __syncwarp();
-  } else if (warp == 7) {
+  } else if (warp == 3) {
     // ------------------------------------------------------------------ PV issuer (CTA 0)
-    // O^T += V^T . P^T: first the tokens of CTA 0 (slots 2n, 2n+1 for half n), a
-    // commit that frees slots 0-3, then the tokens of CTA 1 (slots 4+2n, 5+2n).
-    if (rank == 0 && lane == 0) {
+    // O^T += V^T . P^T: first the tokens of CTA 0 (slots 2n, 2n+1 for half n), then
+    // those of CTA 1 (slots 4+2n, 5+2n), each pair of slots freed by its commit.
+    if (rank == 0) {
+      const uint32_t el = elect_one();
       const uint32_t idesc_pv = idesc_bf16_f32(256, 128, true, false);
       const uint64_t vd0 = smem_desc(sb0 + kOffL, kChunk, 1024, kSwizzle128B);
       const uint64_t pd0 = smem_desc(sb0 + kOffP, 16, 1024, kSwizzle128B);
       bool ok = true;
       for (int j = 0; j < ntiles && ok; ++j) {
         const int s = j & 1;
-        ok = mbar_wait_cluster(bar(B_XF + s), (j >> 1) & 1) && mbar_wait_cluster(bar(B_PFULL + s), (j >> 1) & 1);
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar(B_XF + s), (j >> 1) & 1) &&
+                                         mbar_wait_cluster(bar(B_PFULL + s), (j >> 1) & 1));
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int hv = 0; hv < 2; ++hv) {
+        for (int i = 0; i < 4; ++i) {        // token half i / 2, dims half n = i % 2
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t vd = desc_advance(vd0, (s * 8 + 4 * hv + 2 * n) * kChunk + kk * 2048);
-              const uint64_t pd = desc_advance(pd0, hv * kChunk + kk * 32);
-              mma_bf16_ss_2sm(tmem + kColO + 128u * n, vd, pd, idesc_pv,
-                              (j > 0 || hv > 0 || kk > 0) ? 1u : 0u);
-            }
-          }
-          mma_commit_2sm_mc(bar((hv == 0 ? B_PVX : B_PVDONE) + s), 3);
+          for (int kk = 0; kk < 4; ++kk)
+            mma_pair(el, tmem + kColO + 128u * (i & 1), desc_advance(vd0, (s * 8 + 2 * i) * kChunk + kk * 2048),
+                     desc_advance(pd0, (i >> 1) * kChunk + kk * 32), idesc_pv, j > 0 || i > 1 || kk > 0);
+          commit_pair(el, bar(B_PV + 4 * s + i));
         }
-        if (*abort_flag) ok = false;
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) ok = false;
       }
-      if (!ok) fail();
+      if (!ok && lane == 0) fail();
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ softmax + epilogue
-    // Two warp sets read each TMEM lane quarter: set 0 (warps 2-5) the first 32
-    // of the lane's 64 tokens, set 1 (warps 8-11) the last 32, so a row's scores
-    // sit with four threads (two token halves x two sets).
+    // Two warp sets read each TMEM lane quarter, 32 of the lane's 64 tokens each,
+    // so a row's scores sit with four threads (two token halves x two sets).
     const int g = warp & 3;
-    const int sset = warp >= 8 ? 1 : 0;
+    const int sset = (warp >> 2) - 1;
     const int L = 32 * g + lane;                // TMEM lane
     const int half = L >> 6, row = L & 63;      // S: this CTA's row, token half
     const int xi = 128 * sset + L;
@@ -426,6 +462,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
     const int* flags = reinterpret_cast<const int*>(ctrl_p + kOffFlags);
     const uint32_t peer = rank ^ 1u;
     const uint32_t peer_flag = map_to_rank(ctrl + kOffFlags + 4u * (uint32_t)(4 * sset + g), peer);
+    // a row's values (two token halves x the sets) reduced to all of its threads
+    auto across = [&](float v, auto op) {
+      xmax[xi] = v;
+      named_bar_sync(2, kSoft);
+      float t = op(xmax[row], xmax[64 + row]);
+#pragma unroll
+      for (int k = 1; k < kSets; ++k) t = op(t, op(xmax[128 * k + row], xmax[128 * k + 64 + row]));
+      return t;
+    };
     const int col = (int)rank * 64 + row;       // this row's column of O^T
     float m_run = -INFINITY, l_part = 0.f;
     bool ab = false;
@@ -437,27 +482,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
 
     for (int j = 0; j < ntiles; ++j) {
       const int sb = j & 1;
-      const int ts = w.t + 64 * half + 32 * sset;              // this thread's first token
+      const int ts = w.t + 64 * half + kTok * sset;            // this thread's first token
       const int base = w.b < 0 ? 0 : p.Lp;
       const bool ok0 = block64(p, w, 0).ok, ok1 = block64(p, w, 1).ok;
       const bool gd = guarded(p, w, ok0, ok1);
       int lim = min(w.end, last_pos - base + 1) - ts;          // tokens [ts, ts + lim) pass all but the mask
       if (!live || (w.b >= 0 && w.b != my_b) || !(half ? ok1 : ok0)) lim = 0;
-      uint32_t vis = 0xffffffffu;                              // the mask over [ts, ts + 32), the same across the warp
-      if (mask) vis = __ballot_sync(0xffffffffu, ts + lane < w.end && mask[base + ts + lane] != 0);
-      if (leader) mbar_arrive_expect_tx(bar(B_AX + sb), 8 * 4);
+      uint32_t vis = kAll;                                     // the mask over [ts, ts + kTok), the same across the warp
+      if (mask) vis = kAll & __ballot_sync(0xffffffffu, ts + lane < w.end && mask[base + ts + lane] != 0);
+      if (leader) mbar_arrive_expect_tx(bar(B_AX + sb), kSoftWarps * 4);
       if (!ab) ab = !mbar_wait_cluster(bar(B_SFULL + sb), (j >> 1) & 1);
       ab = __any_sync(0xffffffffu, ab);
-      const uint32_t s_addr = tmem + lane_base + kColS + 64u * sb + 32u * sset;
+      const uint32_t s_addr = tmem + lane_base + kColS + 64u * sb + (uint32_t)(kTok * sset);
       const float m_sub = m_run == -INFINITY ? 0.f : m_run;
-      float e[32];
+      float e[kTok];
       auto load_scores = [&]() {
-        uint32_t v[2][16];
-        tmem_ld16(s_addr, v[0]);
-        tmem_ld16(s_addr + 16u, v[1]);
+        uint32_t v[kTok / 16][16];
+#pragma unroll
+        for (int c = 0; c < kTok / 16; ++c) tmem_ld16(s_addr + 16u * c, v[c]);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 32; ++c) e[c] = __uint_as_float(v[c >> 4][c & 15]);
+        for (int c = 0; c < kTok; ++c) e[c] = __uint_as_float(v[c / 16][c % 16]);
       };
       if (!ab) {
         tc_fence_after();
@@ -465,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
       } else {
         lim = 0;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) e[c] = 0.f;
+        for (int c = 0; c < kTok; ++c) e[c] = 0.f;
       }
       tc_fence_before();
       // a non-finite score among the tile's tokens: a non-finite key (guarded tiles)
@@ -473,37 +518,37 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
       if (gd) {
         float acc = 0.f;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) acc += c < w.end - ts ? e[c] * 0.f : 0.f;
+        for (int c = 0; c < kTok; ++c) acc += c < w.end - ts ? e[c] * 0.f : 0.f;
         odd = !(acc == 0.f);
       }
       // log2 units relative to the row's reference, masked
-      const bool whole = __all_sync(0xffffffffu, lim >= 32) && vis == 0xffffffffu;
+      const bool whole = __all_sync(0xffffffffu, lim >= kTok) && vis == kAll;
       float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       auto scale_scores = [&](float sub) {
         if (whole) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) e[c] = fmaf(e[c], sl2, -sub);
+          for (int c = 0; c < kTok; ++c) e[c] = fmaf(e[c], sl2, -sub);
         } else {
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
+          for (int c = 0; c < kTok; ++c)
             e[c] = (c < lim && ((vis >> c) & 1u)) ? fmaf(e[c], sl2, -sub) : -INFINITY;
         }
       };
       scale_scores(m_sub);
 #pragma unroll
-      for (int c = 0; c < 32; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], e[c]);
+      for (int c = 0; c < kTok; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], e[c]);
       const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
       // the row's reference has to move: its first visible score, or one far above it
       const bool need = m_run == -INFINITY ? mx > -INFINITY : mx > kMove;
       const bool warp_need = __any_sync(0xffffffffu, need);
-      if (lane == 0) st_async_b32(peer_flag + 32u * (uint32_t)(j & 3), warp_need ? 1u : 0u, map_to_rank(bar(B_AX + sb), peer));
+      if (lane == 0) st_async_b32(peer_flag + 4u * kSoftWarps * (uint32_t)sb, warp_need ? 1u : 0u, map_to_rank(bar(B_AX + sb), peer));
 
       float psum;
-      uint32_t pk[16];
+      uint32_t pk[kTok / 2];
       auto weights = [&]() {
         float ps4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
+        for (int c = 0; c < kTok / 2; ++c) {
           const float p0 = fast_exp2(e[2 * c]), p1 = fast_exp2(e[2 * c + 1]);
           ps4[c & 3] += p0 + p1;
           pk[c] = pack_bf16(p0, p1);
@@ -513,33 +558,31 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
       uint8_t* prow = smem + kOffP + half * kChunk + row * 128;
       auto store_weights = [&]() {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint4*>(prow + 16 * ((4 * sset + c) ^ (row & 7))) =
+        for (int c = 0; c < kTok / 8; ++c)
+          *reinterpret_cast<uint4*>(prow + 16 * ((kTok / 8 * sset + c) ^ (row & 7))) =
               make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
         fence_proxy_async_smem();
       };
       weights();
       // the P buffer (and O^T) are free once PV(j-1) is done
-      if (j >= 1 && !ab) ab = !mbar_wait_cluster(bar(B_PVDONE + (sb ^ 1)), ((j - 1) >> 1) & 1);
+      if (j >= 1 && !ab) ab = !mbar_wait_cluster(bar(B_PV + 4 * (sb ^ 1) + 3), ((j - 1) >> 1) & 1);
       store_weights();
       if (!ab) ab = !mbar_wait_cluster(bar(B_AX + sb), (j >> 1) & 1);
       bool peer_need = false;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) peer_need = peer_need || flags[8 * (j & 3) + k] != 0;
-      if (bar_or(1, 256, need || odd || peer_need || ab)) {
+      for (int k = 0; k < kSoftWarps; ++k) peer_need = peer_need || flags[kSoftWarps * sb + k] != 0;
+      if (bar_or(1, kSoft, need || odd || peer_need || ab)) {
         // the rare tile: a reference moves in one of the CTAs (the first tile a
         // row sees), or a non-finite key has to be silenced
-        if (bar_or(1, 256, ab)) {
+        if (bar_or(1, kSoft, ab)) {
           ab = true;
           break;
         }
-        const bool move = bar_or(1, 256, need || peer_need);   // both CTAs agree
-        const bool dirty = bar_or(1, 256, odd);
+        const bool move = bar_or(1, kSoft, need || peer_need);   // both CTAs agree
+        const bool dirty = bar_or(1, kSoft, odd);
         if (move) {
           if (leader) mbar_arrive_expect_tx(bar(B_AL), 64 * 4);
-          xmax[xi] = mx + m_sub;
-          named_bar_sync(2, 256);
-          const float m_all = fmaxf(fmaxf(xmax[xi], xmax[xi ^ 64]), fmaxf(xmax[xi ^ 128], xmax[xi ^ 192]));
+          const float m_all = across(mx + m_sub, [](float a, float b) { return fmaxf(a, b); });
           const bool mv = m_run == -INFINITY ? m_all > -INFINITY : m_all > m_run + kMove;
           const float alpha = mv && m_run != -INFINITY ? exp2f(m_run - m_all) : 1.f;
           if (mv) m_run = m_all;
@@ -556,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
           if (!ab) ab = !mbar_wait_cluster(bar(B_AL), moves & 1);
           ++moves;
           ab = __any_sync(0xffffffffu, ab);
-          named_bar_sync(2, 256);
+          named_bar_sync(2, kSoft);
           if (j > 0 && !ab) {
             tc_fence_after();
             // set n rescales half n
@@ -581,14 +624,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
             if ((u & 0x7f800000u) == 0x7f800000u) u &= 0xffffu;
             return u;
           };
-          for (int i = xi; i < 8 * kChunk / 16; i += 256) {
+          for (int i = xi; i < 8 * kChunk / 16; i += kSoft) {
             const uint4 u = v[i];
             v[i] = make_uint4(keep(u.x), keep(u.y), keep(u.z), keep(u.w));
           }
           fence_proxy_async_smem();
         }
         tc_fence_before();
-        named_bar_sync(2, 256);
+        named_bar_sync(2, kSoft);
       }
       l_part += psum;
       if (gd) {
@@ -601,10 +644,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
 
     // ---------------------------------------------------------------- epilogue
     // the rows' denominators, then each row's output scale to both CTAs
-    ab = bar_or(1, 256, ab);
-    xmax[xi] = l_part;
-    named_bar_sync(2, 256);
-    const float l_tot = (xmax[row] + xmax[64 + row]) + (xmax[128 + row] + xmax[192 + row]);
+    ab = bar_or(1, kSoft, ab);
+    const float l_tot = across(l_part, [](float a, float b) { return a + b; });
     const bool split = p.num_splits > 1;
     const bool seen = !(m_run == -INFINITY && l_tot == 0.f);   // a NaN denominator stays one
     float scale_o = seen ? 1.f / l_tot : 0.f;
@@ -630,10 +671,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
           p.lse[r] = lse;
       }
     }
-    if (ntiles > 0 && !ab) ab = !mbar_wait_cluster(bar(B_PVDONE + ((ntiles - 1) & 1)), ((ntiles - 1) >> 1) & 1);
+    if (ntiles > 0 && !ab) ab = !mbar_wait_cluster(bar(B_PV + 4 * ((ntiles - 1) & 1) + 3), ((ntiles - 1) >> 1) & 1);
     if (!ab) ab = !mbar_wait_cluster(bar(B_EPX), 0);
     ab = __any_sync(0xffffffffu, ab);
-    ab = bar_or(1, 256, ab);
+    ab = bar_or(1, kSoft, ab);
     if (ab) fail();
     tc_fence_after();
     const bool have_o = ntiles > 0 && !ab;
@@ -642,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
     // shared memory (the free tile slots), so the output goes out as 16-byte
     // stores of whole 64- or 128-byte row pieces.
     uint8_t* stage = smem + kOffL + (4 * sset + g) * 2048;   // 16 rows x 32 dims x 4 B per warp
-    const int n = sset;
+    const int n = sset;                                      // set n stores half n
     const int d0 = 256 * n + 128 * (int)rank + 32 * g;       // this warp's first dim
 #pragma unroll 1
     for (int c0 = 0; c0 < kRowsT && r0 + c0 < p.N; c0 += 16) {
@@ -722,12 +763,16 @@ bool encode(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, co
 }
 
 // rows of one source: `outer` sequences or pages of `rows` rows
-bool encode_source(CUtensorMap* kv, CUtensorMap* pe, const void* kvp, const void* pep, int64_t kv_row, int64_t pe_row,
+bool encode_source(CUtensorMap* kv, CUtensorMap* kx, CUtensorMap* pe, const void* kvp, const void* pep, int64_t kv_row, int64_t pe_row,
                    uint64_t kv_outer, uint64_t pe_outer, uint64_t rows, uint64_t outer, int Dr) {
+  const uint64_t d4[4] = {64, rows, 8, outer};
+  const uint64_t s4[3] = {(uint64_t)kv_row * 2, 128, kv_outer * 2};
+  const uint32_t b4[4] = {64, 64, 2, 1};
+  if (!encode(kv, kvp, 4, d4, s4, b4)) return false;
   const uint64_t d[5] = {64, rows, 4, 2, outer};
   const uint64_t s[4] = {(uint64_t)kv_row * 2, 128, 512, kv_outer * 2};
   const uint32_t bx[5] = {64, 64, 2, 2, 1};
-  if (!encode(kv, kvp, 5, d, s, bx)) return false;
+  if (!encode(kx, kvp, 5, d, s, bx)) return false;
   if (Dr == 0) return true;
   const uint64_t dp[3] = {(uint64_t)Dr, rows, outer};
   const uint64_t sp[2] = {(uint64_t)pe_row * 2, pe_outer * 2};
@@ -773,14 +818,14 @@ cudaError_t launch_prefix_sm100(const PrefixParams& p, cudaStream_t st) {
   }
   if (p.Lp > 0) {
     const uint64_t rows = p.ptable ? p.page_size : p.Lp;
-    if (!encode_source(&P.tm_kv[0], &P.tm_pe[0], p.pkv, p.ppe, p.pkv_row, p.ppe_row, rows * p.pkv_row,
+    if (!encode_source(&P.tm_kv[0], &P.tm_kx[0], &P.tm_pe[0], p.pkv, p.ppe, p.pkv_row, p.ppe_row, rows * p.pkv_row,
                        rows * p.ppe_row, rows, p.ptable ? p.p_pages : 1, p.Dr))
       return cudaErrorInvalidValue;
   }
   if (p.Lk > 0) {
     const uint64_t rows = p.table ? p.page_size : p.Lk;
     const bool dense = p.table || p.B == 1;      // the batch stride is unused
-    if (!encode_source(&P.tm_kv[1], &P.tm_pe[1], p.kv, p.pe, p.kv_row, p.pe_row,
+    if (!encode_source(&P.tm_kv[1], &P.tm_kx[1], &P.tm_pe[1], p.kv, p.pe, p.kv_row, p.pe_row,
                        dense ? rows * p.kv_row : (uint64_t)p.kv_batch, dense ? rows * p.pe_row : (uint64_t)p.pe_batch,
                        rows, p.table ? p.num_pages : p.B, p.Dr))
       return cudaErrorInvalidValue;
