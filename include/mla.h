@@ -486,6 +486,8 @@ mla_status_t mla_prefix_decode(const mla_prefix_args* a, void* workspace, size_t
  *   K a multiple of 512; any B, Q, G, N. x and w 16-byte aligned.
  *   workspace: mla_fp4_linear_workspace_size(a) bytes, 256-byte aligned (may
  *       be NULL when that is 0). It is written before it is read in every call.
+ *   err_flag: optional device int32; MLA_DEVICE_ERR_TIMEOUT when a bounded wait
+ *       inside the kernel gave up (the output is then not valid).
  */
 typedef struct mla_fp4_linear_args {
   int B, Q, G, N, K;
@@ -494,6 +496,7 @@ typedef struct mla_fp4_linear_args {
   const void* w;
   float scale;
   void* out;
+  int32_t* err_flag;       /* optional device status word */
 } mla_fp4_linear_args;
 
 size_t mla_fp4_linear_workspace_size(const mla_fp4_linear_args* a);

@@ -8,7 +8,7 @@
 
 namespace mla {
 
-size_t fp4_linear_workspace_bytes(const mla_fp4_linear_args* a, int sms);
+size_t fp4_linear_workspace_bytes(const mla_fp4_linear_args* a);
 cudaError_t launch_fp4_linear(const mla_fp4_linear_args* a, void* ws, int sms, cudaStream_t st);
 
 }  // namespace mla

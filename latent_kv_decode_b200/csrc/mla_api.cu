@@ -588,7 +588,8 @@ mla_status_t validate_fp4_linear(const mla_fp4_linear_args* a) {
   if (!a) return MLA_ERR_INVALID_ARG;
   if (a->B <= 0 || a->Q <= 0 || a->G <= 0 || a->N <= 0 || a->K <= 0) return MLA_ERR_INVALID_ARG;
   if (!a->x || !a->w || !a->out) return MLA_ERR_INVALID_ARG;
-  if (!aligned(a->x, 16) || !aligned(a->w, 16) || !aligned(a->out, 4)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(a->x, 16) || !aligned(a->w, 16) || !aligned(a->out, 2) || !aligned(a->err_flag, 4))
+    return MLA_ERR_INVALID_ARG;
   if (!isfinite(a->scale)) return MLA_ERR_INVALID_ARG;
   for (int64_t s : {a->x_batch_stride, a->x_token_stride, a->x_group_stride, a->x_block_stride})
     if (s < 0 || s % 8 != 0) return MLA_ERR_INVALID_ARG;
@@ -601,14 +602,14 @@ mla_status_t validate_fp4_linear(const mla_fp4_linear_args* a) {
 }  // namespace
 
 extern "C" size_t mla_fp4_linear_workspace_size(const mla_fp4_linear_args* a) {
-  return validate_fp4_linear(a) != MLA_OK ? 0 : mla::fp4_linear_workspace_bytes(a, sm_count());
+  return validate_fp4_linear(a) != MLA_OK ? 0 : mla::fp4_linear_workspace_bytes(a);
 }
 
 extern "C" mla_status_t mla_fp4_linear(const mla_fp4_linear_args* a, void* workspace, size_t workspace_bytes,
                                        void* stream) {
   mla_status_t s = validate_fp4_linear(a);
   if (s != MLA_OK) return s;
-  const size_t need = mla::fp4_linear_workspace_bytes(a, sm_count());
+  const size_t need = mla::fp4_linear_workspace_bytes(a);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return MLA_ERR_WORKSPACE;
   return cuda_status(mla::launch_fp4_linear(a, workspace, sm_count(), (cudaStream_t)stream));
 }

@@ -173,7 +173,7 @@ class Fp4LinearArgs(ctypes.Structure):
         ("x", _c.c_void_p),
         ("x_batch_stride", _c.c_int64), ("x_token_stride", _c.c_int64),
         ("x_group_stride", _c.c_int64), ("x_block_stride", _c.c_int64),
-        ("w", _c.c_void_p), ("scale", _c.c_float), ("out", _c.c_void_p),
+        ("w", _c.c_void_p), ("scale", _c.c_float), ("out", _c.c_void_p), ("err_flag", _c.c_void_p),
     ]
 
 
