@@ -493,77 +493,89 @@ def mla_group_wo(x, wo_a, wo_b=None, *, stream=None, **kw) -> torch.Tensor:
 
 
 # --- the step on raw projection outputs, shared prefixes and FP4 weights -----
+#
+# These calls are small next to the GPU's work only while the host stays out of
+# the way, so their checks read each tensor property once.
 
-def _need(cond: bool, what: str) -> None:
-    if not cond:
-        raise MlaError(what)
-
-
-def _int32(t, name: str, n: Optional[int] = None) -> None:
-    """``t`` (None allowed) is a contiguous int32 tensor, of ``n`` elements when given."""
-    if t is not None:
-        _need(t.dtype == torch.int32 and t.is_contiguous(), f"{name} must be contiguous int32")
-        _need(n is None or t.numel() == n, f"{name} must have {n} elements")
-
-
-def _one_device(first: torch.Tensor, *ts) -> None:
-    _need_cuda(first, *ts)
+def _same_device(dev: int, *ts) -> None:
+    if dev < 0:
+        raise MlaError("libmla takes CUDA tensors only")
     for t in ts:
-        _need(t is None or t.device == first.device, "tensors are on different devices")
+        if t is not None and t.get_device() != dev:
+            raise MlaError("libmla takes CUDA tensors of one device")
 
 
-class _on:
-    """The device and stream of a call: ``t``'s device is current inside, and
-    ``.stream`` is ``stream`` or that device's current stream. Memory allocated
-    for the call is tied to that stream with :meth:`used`."""
-
-    def __init__(self, t: torch.Tensor, stream):
-        self.device, self.given = t.device, stream
-
-    def __enter__(self):
-        self._guard = torch.cuda.device(self.device)
-        self._guard.__enter__()
-        current = torch.cuda.current_stream(self.device)
-        self.stream = _stream(current if self.given is None else self.given)
-        self._other = self.stream != current.cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        return self._guard.__exit__(*exc)
-
-    def used(self, *ts) -> None:
-        if self._other:
-            s = torch.cuda.ExternalStream(self.stream, device=self.device)
-            for t in ts:
-                if t is not None:
-                    t.record_stream(s)
+def _int32(t: torch.Tensor, name: str) -> int:
+    """Device pointer of a contiguous int32 tensor."""
+    if t.dtype is not torch.int32 or not t.is_contiguous():
+        raise MlaError(f"{name} must be contiguous int32")
+    return t.data_ptr()
 
 
-def _cache_fields(a, kv_cache, pe_cache, block_table, page_size: int, Lk: Optional[int], B: int) -> None:
-    """Fill the cache part of an argument struct: (B, Lk, C) views, or
-    (num_pages, page_size, C) pools with a (B, max_pages) ``block_table``."""
-    for t in (kv_cache, pe_cache):
-        _need(t is None or (t.dim() == 3 and t.stride(-1) == 1), "cache tensors are 3-D with a packed last dim")
-    a.kv_cache, a.pe_cache = _ptr(kv_cache), _ptr(pe_cache)
-    a.kv_row_stride, a.kv_batch_stride = kv_cache.stride(1), kv_cache.stride(0)
-    if pe_cache is not None:
-        _need(pe_cache.shape[:2] == kv_cache.shape[:2], "kv_cache and pe_cache hold different rows")
-        a.pe_row_stride, a.pe_batch_stride = pe_cache.stride(1), pe_cache.stride(0)
-    if block_table is not None:
-        _int32(block_table, "block_table")
-        _need(block_table.dim() == 2 and block_table.shape[0] == B, "block_table must be (B, max_pages)")
-        _need(kv_cache.shape[1] == page_size, "the pool's pages must have page_size rows")
-        for t in (kv_cache, pe_cache):
-            _need(t is None or t.shape[0] == 1 or t.stride(0) == page_size * t.stride(1),
-                  "a pool's pages must follow each other")
-        a.block_table = _ptr(block_table)
-        a.max_pages, a.page_size, a.num_pages = block_table.shape[1], page_size, kv_cache.shape[0]
-        a.kv_batch_stride = a.pe_batch_stride = 0
-        a.Lk = Lk if Lk is not None else a.max_pages * page_size
+def _launch(fn, dev: int, stream, *made):
+    """Call ``fn(stream handle)`` with device ``dev`` current, on ``stream`` or that
+    device's current stream; memory ``made`` for the call is tied to a stream
+    that is not the current one."""
+    current = torch._C._cuda_getCurrentRawStream(dev)
+    handle = current if stream is None else _stream(stream)
+    if torch.cuda.current_device() == dev:
+        r = fn(handle)
     else:
-        _need(kv_cache.shape[0] == B, "a contiguous cache must be (B, Lk, C)")
-        a.Lk = Lk if Lk is not None else kv_cache.shape[1]
-        _need(a.Lk <= kv_cache.shape[1], "Lk is beyond the cache's rows")
+        with torch.cuda.device(dev):
+            r = fn(handle)
+    if handle != current:
+        s = torch.cuda.ExternalStream(handle, device=dev)
+        for t in made:
+            if t is not None:
+                t.record_stream(s)
+    return r
+
+
+def _cache_rows(kv_cache, pe_cache, block_table, page_size: int, Lk: Optional[int], B: int, Ckv: int, Dr: int):
+    """(kv row stride, pe row stride, kv batch stride, pe batch stride, Lk, table, max_pages, num_pages) of
+    (B, Lk, C) views, or of (num_pages, page_size, C) pools with a (B, max_pages) ``block_table``."""
+    n0, n1, width = kv_cache.shape
+    kb, kr, k1 = kv_cache.stride()
+    pb = pr = 0
+    if Dr:
+        if pe_cache is None or pe_cache.dim() != 3:
+            raise MlaError("pe_cache must be 3-D")
+        m0, m1, pwidth = pe_cache.shape
+        pb, pr, p1 = pe_cache.stride()
+        if m0 != n0 or m1 != n1 or pwidth < Dr or p1 != 1:
+            raise MlaError("pe_cache must hold kv_cache's rows, at least Dr wide, last dim packed")
+    if width < Ckv or k1 != 1:
+        raise MlaError("kv_cache rows must be at least 512 wide, last dim packed")
+    if block_table is None:
+        if n0 != B:
+            raise MlaError("a contiguous cache must be (B, Lk, C)")
+        if Lk is None:
+            Lk = n1
+        elif Lk > n1:
+            raise MlaError("Lk is beyond the cache's rows")
+        return kr, pr, kb, pb, Lk, None, 0, 0
+    table = _int32(block_table, "block_table")
+    rows, max_pages = block_table.shape
+    if rows != B or n1 != page_size:
+        raise MlaError("block_table must be (B, max_pages), and the pool's pages of page_size rows")
+    if n0 > 1 and (kb != n1 * kr or (Dr and pb != n1 * pr)):
+        raise MlaError("a pool's pages must follow each other")
+    return kr, pr, 0, 0, max_pages * page_size if Lk is None else Lk, table, max_pages, n0
+
+
+def _step(t: torch.Tensor, uniform: bool) -> int:
+    """Stride from token to token of (N, ...) or (B, Q, ...) rows with a packed last dim."""
+    st = t.stride()
+    if st[-1] != 1:
+        raise MlaError("mla_rope_append: the last dim must be packed")
+    if not uniform:
+        return st[0]
+    B, Q = t.shape[:2]
+    if Q == 1:
+        return st[0]
+    if B > 1 and st[0] != Q * st[1]:
+        raise MlaError("mla_rope_append: tokens must step evenly")
+    return st[1]
 
 
 def make_rope_append_args(c_kv, k_pe, kv_cache, pe_cache, seq_lens, *, q_pe=None, q_out=None, cu_tokens=None,
@@ -577,53 +589,49 @@ def make_rope_append_args(c_kv, k_pe, kv_cache, pe_cache, seq_lens, *, q_pe=None
     (slices of wider projection rows); the tokens of c_kv, k_pe and q_pe must
     step evenly.
     """
-    _one_device(c_kv, k_pe, kv_cache, pe_cache, seq_lens, q_pe, q_out, cu_tokens, block_table, err_flag)
-    _need(all(t.dtype == c_kv.dtype for t in (k_pe, kv_cache, pe_cache, q_pe, q_out) if t is not None),
-          "mla_rope_append: tensors must share one dtype")
+    _same_device(c_kv.get_device(), k_pe, kv_cache, pe_cache, seq_lens, q_pe, q_out, cu_tokens, block_table, err_flag)
+    dtype = c_kv.dtype
+    if not (k_pe.dtype is dtype and kv_cache.dtype is dtype and pe_cache.dtype is dtype and
+            (q_pe is None or q_pe.dtype is dtype) and (q_out is None or q_out.dtype is dtype)):
+        raise MlaError("mla_rope_append: tensors must share one dtype")
     B = seq_lens.numel()
-    _int32(seq_lens, "seq_lens")
-    _int32(cu_tokens, "cu_tokens", B + 1)
-    _int32(err_flag, "err_flag")
-    a = RopeAppendArgs()
-    lead = 1 if cu_tokens is not None else 2
-    _need(c_kv.dim() == lead + 1 and k_pe.dim() == lead + 1 and k_pe.shape[:-1] == c_kv.shape[:-1],
-          "mla_rope_append: c_kv and k_pe must hold the same tokens")
-    _need(lead == 1 or c_kv.shape[0] == B, "mla_rope_append: c_kv must be (B, Q, 512)")
-    a.B, a.Ckv, a.Dr, a.dtype = B, c_kv.shape[-1], k_pe.shape[-1], _qdtype(c_kv)
-    a.N = c_kv.shape[:-1].numel()
-    a.Q = c_kv.shape[1] if lead == 2 else 0
-
-    def token_stride(t: torch.Tensor) -> int:
-        _need(t.stride(-1) == 1, "mla_rope_append: the last dim must be packed")
-        if lead == 1:
-            return t.stride(0)
-        s = t.stride(1) if t.shape[1] > 1 else t.stride(0)
-        _need(t.shape[0] == 1 or t.shape[1] == 1 or t.stride(0) == t.shape[1] * s,
-              "mla_rope_append: tokens must step evenly")
-        return s
-
-    a.c_kv, a.k_pe = _ptr(c_kv), _ptr(k_pe)
-    a.c_kv_stride, a.k_pe_stride = token_stride(c_kv), token_stride(k_pe)
+    uniform = cu_tokens is None
+    cu = None
+    if not uniform:
+        cu = _int32(cu_tokens, "cu_tokens")
+        if cu_tokens.numel() != B + 1:
+            raise MlaError("cu_tokens must have B + 1 elements")
+    *tokens, Ckv = c_kv.shape
+    *same, Dr = k_pe.shape
+    if same != tokens or len(tokens) != 1 + uniform or (uniform and tokens[0] != B):
+        raise MlaError("mla_rope_append: c_kv and k_pe must be (B, Q, C), or (N, C) with cu_tokens")
+    N, Q = (B * tokens[1], tokens[1]) if uniform else (tokens[0], 0)
+    H = qs = qh = ob = ot = oh = 0
+    qp = op = None
     if q_pe is not None:
-        _need(q_pe.dim() == lead + 2 and q_pe.shape[:lead] == c_kv.shape[:-1] and q_pe.shape[-1] == a.Dr,
-              "mla_rope_append: q_pe must hold the tokens' heads, Dr wide")
-        a.H = q_pe.shape[-2]
-        shape = tuple(q_pe.shape) if lead == 1 else (B, a.H, a.Q, a.Dr)
+        *same, H, width = q_pe.shape
+        if same != tokens or width != Dr:
+            raise MlaError("mla_rope_append: q_pe must hold the tokens' heads, Dr wide")
+        shape = (B, H, Q, Dr) if uniform else (N, H, Dr)
         if q_out is None:
-            q_out = torch.empty(shape, dtype=q_pe.dtype, device=q_pe.device)
-        _need(tuple(q_out.shape) == shape and q_out.stride(-1) == 1, f"mla_rope_append: q_out must be {shape}")
-        a.q_pe, a.q_out = _ptr(q_pe), _ptr(q_out)
-        a.q_token_stride, a.q_head_stride = token_stride(q_pe), q_pe.stride(-2)
-        if lead == 1:
-            a.o_token_stride, a.o_head_stride = q_out.stride(0), q_out.stride(1)
+            q_out = torch.empty(shape, dtype=dtype, device=q_pe.device)
+        elif tuple(q_out.shape) != shape or q_out.stride(-1) != 1:
+            raise MlaError(f"mla_rope_append: q_out must be {shape}, last dim packed")
+        qs, qh = _step(q_pe, uniform), q_pe.stride(-2)
+        if uniform:
+            ob, oh, ot, _ = q_out.stride()
         else:
-            a.o_batch_stride, a.o_head_stride, a.o_token_stride = q_out.stride()[:3]
-    else:
-        _need(q_out is None, "mla_rope_append: q_out without q_pe")
-    _cache_fields(a, kv_cache, pe_cache, block_table, page_size, Lk, B)
-    _need(kv_cache.shape[-1] >= a.Ckv and pe_cache.shape[-1] >= a.Dr, "mla_rope_append: cache rows are too narrow")
-    a.seq_lens, a.cu_tokens, a.err_flag = _ptr(seq_lens), _ptr(cu_tokens), _ptr(err_flag)
-    a.pos_offset, a.rope_theta = int(pos_offset), float(rope_theta)
+            ot, oh, _ = q_out.stride()
+        qp, op = q_pe.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise MlaError("mla_rope_append: q_out without q_pe")
+    kr, pr, kb, pb, Lk, table, max_pages, num_pages = _cache_rows(kv_cache, pe_cache, block_table, page_size, Lk, B,
+                                                                  Ckv, Dr)
+    a = RopeAppendArgs(B, Q, N, Ckv, Dr, H, _qdtype(c_kv), c_kv.data_ptr(), k_pe.data_ptr(), qp, op,
+                       _step(c_kv, uniform), _step(k_pe, uniform), qs, qh, ob, ot, oh, kv_cache.data_ptr(),
+                       pe_cache.data_ptr(), kr, pr, kb, pb, Lk, _int32(seq_lens, "seq_lens"), table, max_pages,
+                       page_size, num_pages, cu, pos_offset, rope_theta,
+                       None if err_flag is None else _int32(err_flag, "err_flag"))
     return a, q_out
 
 
@@ -636,9 +644,10 @@ def mla_rope_append(c_kv, k_pe, kv_cache, pe_cache, seq_lens, *, stream=None, **
     stored and sets DEVICE_ERR_BLOCK_TABLE in ``err_flag``.
     """
     a, q_out = make_rope_append_args(c_kv, k_pe, kv_cache, pe_cache, seq_lens, **kw)
-    with _on(c_kv, stream) as on:
-        _check(lib().mla_rope_append(ctypes.byref(a), on.stream), "mla_rope_append")
-        on.used(q_out)
+    L = lib()
+    status = _launch(lambda st: L.mla_rope_append(ctypes.byref(a), st), c_kv.get_device(), stream, q_out)
+    if status:
+        _check(status, "mla_rope_append")
     return q_out
 
 
@@ -649,9 +658,10 @@ class PrefixCall:
     args: PrefixArgs
     num_splits: int
     workspace: Optional[torch.Tensor]
+    workspace_bytes: int
     x: torch.Tensor
     lse: Optional[torch.Tensor]
-    keep: list = field(default_factory=list)   # tensors the pointers in args refer to
+    keep: tuple = ()   # tensors the pointers in args refer to
 
 
 def make_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, softmax_scale: float, *,
@@ -666,89 +676,115 @@ def make_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, so
     kv_cache / pe_cache: the sequences' own tokens, laid out as for mla_decode,
     or None (no own tokens). ``causal_mask`` covers prefix_len + Lk positions.
     """
-    _one_device(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, prefix_table, seq_lens, block_table,
-                causal_mask, sinks, x, lse, workspace, err_flag)
-    _need(q_lat.dim() == 4 and q_lat.is_contiguous(), "q_lat must be contiguous (B, H, Q, 512)")
-    B, H, Q, Ckv = q_lat.shape
-    _need(q_pe is None or (q_pe.is_contiguous() and q_pe.shape[:3] == q_lat.shape[:3]),
-          "q_pe must be contiguous (B, H, Q, Dr)")
-    a = PrefixArgs()
-    a.B, a.H, a.Q, a.Ckv = B, H, Q, Ckv
-    a.Dr = 0 if q_pe is None else q_pe.shape[-1]
-    a.dtype = _qdtype(q_lat)
+    dev = q_lat.get_device()
+    _same_device(dev, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, prefix_table, seq_lens, block_table,
+                 causal_mask, sinks, x, lse, workspace, err_flag)
+    dtype = q_lat.dtype
     for t in (q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, x):
-        _need(t is None or t.dtype == q_lat.dtype, "mla_prefix_decode: tensors must share one dtype")
-    a.q_lat, a.q_pe = _ptr(q_lat), _ptr(q_pe)
-    for t, w in ((prefix_kv, Ckv), (prefix_pe, a.Dr), (kv_cache, Ckv), (pe_cache, a.Dr)):
-        _need(t is None or t.shape[-1] >= w, "mla_prefix_decode: cache rows are too narrow")
-    _int32(prefix_table, "prefix_table")
-    if prefix_kv is not None:
-        dim = 2 if prefix_table is None else 3
-        _need(prefix_kv.dim() == dim and prefix_kv.stride(-1) == 1, f"prefix_kv must be {dim}-D, last dim packed")
-        a.prefix_kv, a.prefix_kv_stride = _ptr(prefix_kv), prefix_kv.stride(-2)
-        if a.Dr:
-            _need(prefix_pe is not None and prefix_pe.stride(-1) == 1 and prefix_pe.shape[:-1] == prefix_kv.shape[:-1],
-                  "prefix_pe must hold prefix_kv's rows")
-            a.prefix_pe, a.prefix_pe_stride = _ptr(prefix_pe), prefix_pe.stride(-2)
-        if prefix_table is None:
-            a.prefix_len = prefix_kv.shape[0] if prefix_len is None else prefix_len
-            _need(a.prefix_len <= prefix_kv.shape[0], "prefix_len is beyond prefix_kv's rows")
-        else:
-            _need(prefix_len is not None, "a paged prefix needs prefix_len")
-            _need(prefix_kv.shape[1] == page_size and prefix_table.numel() * page_size >= prefix_len,
-                  "prefix_table or page_size does not cover prefix_len")
-            for t in (prefix_kv, prefix_pe):
-                _need(t is None or t.shape[0] == 1 or t.stride(0) == page_size * t.stride(1),
-                      "a pool's pages must follow each other")
-            a.prefix_len, a.prefix_table, a.prefix_num_pages = prefix_len, _ptr(prefix_table), prefix_kv.shape[0]
+        if t is not None and t.dtype is not dtype:
+            raise MlaError("mla_prefix_decode: tensors must share one dtype")
+    B, H, Q, Ckv = shape = q_lat.shape
+    Dr, qp = 0, None
+    if q_pe is not None:
+        *same, Dr = q_pe.shape
+        qp = q_pe.data_ptr()
+        if same != [B, H, Q] or not q_pe.is_contiguous():
+            raise MlaError("q_pe must be contiguous (B, H, Q, Dr)")
+    if not q_lat.is_contiguous():
+        raise MlaError("q_lat must be contiguous (B, H, Q, 512)")
+
+    pk = pp = ptab = None
+    pks = pps = p_pages = 0
+    if prefix_kv is None:
+        if prefix_len:
+            raise MlaError("prefix_len without prefix_kv")
+        prefix_len = 0
     else:
-        _need(not prefix_len, "prefix_len without prefix_kv")
-    a.page_size = page_size
+        paged = prefix_table is not None
+        *rows, width = prefix_kv.shape
+        st = prefix_kv.stride()
+        pk, pks = prefix_kv.data_ptr(), st[-2]
+        if len(rows) != 1 + paged or width < Ckv or st[-1] != 1:
+            raise MlaError("prefix_kv must be (rows, C), or (pages, page_size, C) with prefix_table, last dim packed")
+        if Dr:
+            *same, width = prefix_pe.shape if prefix_pe is not None else (0,)
+            if same != rows or width < Dr or prefix_pe.stride(-1) != 1:
+                raise MlaError("prefix_pe must hold prefix_kv's rows, at least Dr wide, last dim packed")
+            pp, pps = prefix_pe.data_ptr(), prefix_pe.stride(-2)
+        if paged:
+            ptab = _int32(prefix_table, "prefix_table")
+            p_pages = rows[0]
+            if prefix_len is None or rows[1] != page_size or prefix_table.numel() * page_size < prefix_len:
+                raise MlaError("a paged prefix needs prefix_len, pages of page_size rows, and a table that covers it")
+            if p_pages > 1 and (st[0] != page_size * pks or (Dr and prefix_pe.stride(0) != page_size * pps)):
+                raise MlaError("a pool's pages must follow each other")
+        elif prefix_len is None:
+            prefix_len = rows[0]
+        elif prefix_len > rows[0]:
+            raise MlaError("prefix_len is beyond prefix_kv's rows")
+
+    k = p = table = None
+    kr = pr = kb = pb = max_pages = num_pages = 0
     if kv_cache is not None:
-        _need(a.Dr == 0 or pe_cache is not None, "pe_cache is missing")
-        _cache_fields(a, kv_cache, pe_cache if a.Dr else None, block_table, page_size, Lk, B)
-    else:
-        _need(not Lk, "Lk without kv_cache")
-    _int32(seq_lens, "seq_lens", B)
-    _int32(err_flag, "err_flag")
-    a.seq_lens = _ptr(seq_lens)
+        kr, pr, kb, pb, Lk, table, max_pages, num_pages = _cache_rows(kv_cache, pe_cache, block_table, page_size, Lk,
+                                                                      B, Ckv, Dr)
+        k, p = kv_cache.data_ptr(), pe_cache.data_ptr() if Dr else None
+    elif Lk:
+        raise MlaError("Lk without kv_cache")
+    Lk = Lk or 0
+    lens = None
+    if seq_lens is not None:
+        lens = _int32(seq_lens, "seq_lens")
+        if seq_lens.numel() != B:
+            raise MlaError("seq_lens must have B elements")
+    mask = None
     if causal_mask is not None:
         causal_mask = causal_mask.reshape(-1).to(torch.uint8).contiguous()
-        _need(causal_mask.numel() >= a.prefix_len + a.Lk, "causal_mask must cover prefix_len + Lk positions")
-        a.causal_mask = _ptr(causal_mask)
-    a.causal, a.softmax_scale, a.num_splits = int(bool(causal)), float(softmax_scale), int(num_splits)
-    if sinks is not None:
-        _need(sinks.dtype == torch.float32 and sinks.is_contiguous() and sinks.numel() == H, "sinks must be (H) float32")
-        a.sinks = _ptr(sinks)
+        mask = causal_mask.data_ptr()
+        if causal_mask.numel() < prefix_len + Lk:
+            raise MlaError("causal_mask must cover prefix_len + Lk positions")
+    if sinks is not None and (sinks.dtype is not torch.float32 or not sinks.is_contiguous() or sinks.numel() != H):
+        raise MlaError("sinks must be (H) float32")
     if x is None:
-        x = torch.empty((B, H, Q, Ckv), dtype=q_lat.dtype, device=q_lat.device)
-    _need(x.is_contiguous() and x.shape == q_lat.shape, "x must be contiguous (B, H, Q, 512)")
-    if lse is None and want_lse:
+        x = torch.empty(shape, dtype=dtype, device=q_lat.device)
+    elif not x.is_contiguous() or x.shape != shape:
+        raise MlaError("x must be contiguous (B, H, Q, 512)")
+    if lse is not None:
+        if lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() != B * H * Q:
+            raise MlaError("lse must be contiguous float32 (B, H, Q)")
+    elif want_lse:
         lse = torch.empty((B, H, Q), dtype=torch.float32, device=q_lat.device)
-    _need(lse is None or (lse.is_contiguous() and lse.dtype == torch.float32 and lse.numel() == B * H * Q),
-          "lse must be contiguous float32 (B, H, Q)")
-    a.x, a.lse, a.err_flag = _ptr(x), _ptr(lse), _ptr(err_flag)
-    with torch.cuda.device(q_lat.device):
-        S = lib().mla_prefix_decode_num_splits(ctypes.byref(a))
-        if S < 0:
-            raise MlaError("mla_prefix_decode arguments rejected (MLA_ERR_INVALID_ARG or MLA_ERR_UNSUPPORTED)")
-        need = int(lib().mla_prefix_decode_workspace_size(ctypes.byref(a)))
-    if need and workspace is None:
+    a = PrefixArgs(B, H, Q, Ckv, Dr, _qdtype(q_lat), q_lat.data_ptr(), qp, pk, pp, pks, pps, prefix_len, ptab, p_pages,
+                   k, p, kr, pr, kb, pb, Lk, lens, table, max_pages, page_size, num_pages, mask, bool(causal),
+                   softmax_scale, _ptr(sinks), num_splits, x.data_ptr(), _ptr(lse),
+                   None if err_flag is None else _int32(err_flag, "err_flag"))
+    L, ref = lib(), ctypes.byref(a)
+    # the split rule reads the current device's SM count
+    if torch.cuda.current_device() == dev:
+        S, need = L.mla_prefix_decode_num_splits(ref), L.mla_prefix_decode_workspace_size(ref)
+    else:
+        with torch.cuda.device(dev):
+            S, need = L.mla_prefix_decode_num_splits(ref), L.mla_prefix_decode_workspace_size(ref)
+    if S < 0:
+        raise MlaError("mla_prefix_decode arguments rejected (MLA_ERR_INVALID_ARG or MLA_ERR_UNSUPPORTED)")
+    if not need:
+        workspace = None
+    elif workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q_lat.device)
-    _need(not need or workspace.numel() * workspace.element_size() >= need, "workspace is too small")
-    keep = [q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, prefix_table, seq_lens, block_table, causal_mask,
-            sinks, err_flag]
-    return PrefixCall(args=a, num_splits=S, workspace=workspace if need else None, x=x, lse=lse, keep=keep)
+    elif not workspace.is_contiguous() or workspace.nbytes < need:
+        raise MlaError(f"mla_prefix_decode needs a contiguous workspace of {need} bytes")
+    return PrefixCall(a, S, workspace, need, x, lse,
+                      (q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, prefix_table, seq_lens, block_table,
+                       causal_mask, sinks, err_flag))
 
 
 def launch_prefix_decode(call: PrefixCall, stream=None):
     """Enqueue a prepared call; returns its (x, lse)."""
-    ws = call.workspace
-    with _on(call.x, stream) as on:
-        _check(lib().mla_prefix_decode(ctypes.byref(call.args), _ptr(ws),
-                                       0 if ws is None else ws.numel() * ws.element_size(), on.stream),
-               "mla_prefix_decode")
-        on.used(call.x, call.lse, ws, *call.keep)
+    ws, L = call.workspace, lib()
+    status = _launch(lambda st: L.mla_prefix_decode(ctypes.byref(call.args), _ptr(ws), call.workspace_bytes, st),
+                     call.x.get_device(), stream, call.x, call.lse, ws, *call.keep)
+    if status:
+        _check(status, "mla_prefix_decode")
     return call.x, call.lse
 
 
@@ -766,99 +802,112 @@ def mla_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, sof
 def mla_prefix_decode_step(q_nope, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, wkv_b, softmax_scale,
                            causal_mask=None, **kw):
     """mla_decode_step behind a shared prefix -> out (B,H,Q,Vd): absorb, prefix decode, up-project."""
-    Dn, stream = q_nope.shape[-1], kw.get("stream")
-    with torch.cuda.device(q_nope.device):
-        q_lat = mla_absorb_q(q_nope, wkv_b, stream=stream)
-        x, _ = mla_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, softmax_scale,
-                                 causal_mask=causal_mask, **kw)
-        out = mla_up_proj(x, wkv_b, Dn, stream=stream)
-    with _on(x, stream) as on:
-        on.used(q_lat, x, out)
+    Dn, stream, dev = q_nope.shape[-1], kw.get("stream"), q_nope.get_device()
+    _same_device(dev, wkv_b)
+
+    def absorb(st):
+        return mla_absorb_q(q_nope, wkv_b, stream=st)
+
+    q_lat = _launch(absorb, dev, stream)
+    x, _ = mla_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, softmax_scale,
+                             causal_mask=causal_mask, **kw)
+    out = _launch(lambda st: mla_up_proj(x, wkv_b, Dn, stream=st), dev, stream, q_lat, x)
+    if stream is not None:
+        _launch(lambda st: None, dev, stream, out)
     return out
 
 
 FP4_BLOCK, FP4_ENTRY_BYTES = 512, 288
 
 
-def pack_fp4_weight(w: torch.Tensor, scale: Optional[float] = None, *, stream=None):
+def pack_fp4_weight(w: torch.Tensor, scale: Optional[float] = None):
     """Weights (..., N, K) as FP4 entries: returns (entries (..., N, K/512, 288) uint8, scale).
 
     ``w / scale`` is quantised by mla_cache_append's FP4 rule (an E4M3 scale per
     16 channels, E2M1 codes), so W ~ scale * value. Without ``scale`` it is chosen
     so that the largest weight meets the format's end (448 * 6); that reads the
-    maximum back to the host. Done once, when weights are loaded.
+    maximum back to the host. Done once, when weights are loaded, on the current
+    stream.
     """
-    _need_cuda(w)
-    _need(w.dim() >= 2 and w.shape[-1] % FP4_BLOCK == 0, "pack_fp4_weight: K must be a multiple of 512")
+    dev = w.get_device()
+    _same_device(dev)
+    if w.dim() < 2 or w.shape[-1] % FP4_BLOCK or not w.is_floating_point() or w.numel() == 0:
+        raise MlaError("pack_fp4_weight: w must be (..., N, K) floating point, K a multiple of 512")
     wf = w.float()
     if scale is None:
         scale = float(wf.abs().max()) / (448.0 * 6.0) or 1.0
     rows = (wf / scale).reshape(1, -1, FP4_BLOCK).contiguous()
     n = rows.shape[1]
-    _need(n < 2 ** 31, "pack_fp4_weight: too many entries")
     entries = torch.empty((1, n, FP4_ENTRY_BYTES), dtype=torch.uint8, device=w.device)
     lens = torch.full((1,), n, dtype=torch.int32, device=w.device)
-    with _on(w, stream) as on:
-        mla_cache_append(rows, None, entries, None, lens, stream=on.stream)
-        on.used(rows, entries, lens)
+    _launch(lambda st: mla_cache_append(rows, None, entries, None, lens, stream=st), dev, None)
     return entries.reshape(*w.shape[:-1], w.shape[-1] // FP4_BLOCK, FP4_ENTRY_BYTES), scale
 
 
-def _fp4_linear(x, a: Fp4LinearArgs, w, scale: float, out, stream):
-    """Check what both callers share, allocate, launch."""
-    _one_device(x, w, out)
-    _need(x.dtype == torch.bfloat16, "mla_fp4_linear takes bf16 activations")
-    _need(w.dtype == torch.uint8 and w.is_contiguous() and w.shape[-1] == FP4_ENTRY_BYTES,
-          "mla_fp4_linear weights are contiguous uint8 entries of 288 bytes")
-    _need(out.dtype == torch.bfloat16 and out.is_contiguous(), "mla_fp4_linear: out must be contiguous bf16")
-    a.x, a.w, a.out, a.scale = _ptr(x), _ptr(w), _ptr(out), float(scale)
-    if x.numel() == 0:
-        return out
-    with _on(x, stream) as on:
-        need = int(lib().mla_fp4_linear_workspace_size(ctypes.byref(a)))
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-        _check(lib().mla_fp4_linear(ctypes.byref(a), _ptr(ws), need, on.stream), "mla_fp4_linear")
-        on.used(ws, out)
+def _fp4_linear(x, w, dims, strides, scale: float, out, err_flag, stream):
+    """One mla_fp4_linear launch; ``dims`` (B, Q, G, N, K), ``strides`` those of x."""
+    dev = x.get_device()
+    _same_device(dev, w, out, err_flag)
+    if x.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16 or not out.is_contiguous():
+        raise MlaError("mla_fp4_linear takes and gives bf16, out contiguous")
+    if w.dtype is not torch.uint8 or not w.is_contiguous() or w.shape[-1] != FP4_ENTRY_BYTES:
+        raise MlaError("mla_fp4_linear weights are contiguous uint8 entries of 288 bytes")
+    if dims[0] * dims[1] == 0:
+        return out                                # no tokens
+    a = Fp4LinearArgs(*dims, x.data_ptr(), *strides, w.data_ptr(), scale, out.data_ptr(),
+                      None if err_flag is None else _int32(err_flag, "err_flag"))
+    L, ref = lib(), ctypes.byref(a)
+    need = L.mla_fp4_linear_workspace_size(ref)
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    status = _launch(lambda st: L.mla_fp4_linear(ref, _ptr(ws), need, st), dev, stream, x, out, ws)
+    if status:
+        _check(status, "mla_fp4_linear")
     return out
 
 
 def mla_fp4_linear(x: torch.Tensor, w: torch.Tensor, scale: float = 1.0, *, out: Optional[torch.Tensor] = None,
-                   stream=None) -> torch.Tensor:
+                   err_flag=None, stream=None) -> torch.Tensor:
     """out[..., n] = scale * sum_k x[..., k] W[n, k]: x (..., K) bf16, w (N, K/512, 288) FP4 entries."""
-    _need(w.dim() == 3 and x.dim() >= 1 and x.shape[-1] == w.shape[1] * FP4_BLOCK,
-          "mla_fp4_linear: w must be (N, K/512, 288) for x (..., K)")
-    N, K = w.shape[0], x.shape[-1]
-    x2 = x.reshape(-1, K)
-    if x2.stride(-1) != 1 or x2.stride(0) % 8 or x2.data_ptr() % 16:
+    *lead, K = x.shape
+    if w.dim() != 3 or K != w.shape[1] * FP4_BLOCK:
+        raise MlaError("mla_fp4_linear: w must be (N, K/512, 288) for x (..., K)")
+    N = w.shape[0]
+    x2 = x if len(lead) == 1 else x.reshape(-1, K)
+    step, one = x2.stride()
+    if one != 1 or step % 8 or x2.data_ptr() % 16:
         x2 = x2.contiguous()
+        step = K
     if out is None:
-        out = torch.empty((*x.shape[:-1], N), dtype=torch.bfloat16, device=x.device)
-    _need(tuple(out.shape) == (*x.shape[:-1], N), "mla_fp4_linear: out has another shape")
-    a = Fp4LinearArgs()
-    a.B, a.Q, a.G, a.N, a.K = x2.shape[0], 1, 1, N, K
-    a.x_batch_stride, a.x_block_stride = x2.stride(0), FP4_BLOCK
-    return _fp4_linear(x2, a, w, scale, out, stream)
+        out = torch.empty((*lead, N), dtype=torch.bfloat16, device=x.device)
+    elif list(out.shape) != [*lead, N]:
+        raise MlaError("mla_fp4_linear: out has another shape")
+    return _fp4_linear(x2, w, (x2.shape[0], 1, 1, N, K), (step, 0, 0, FP4_BLOCK), scale, out, err_flag, stream)
 
 
 def mla_fp4_group_wo(x: torch.Tensor, wo_a: torch.Tensor, wo_b: Optional[torch.Tensor] = None, *,
                      scale_a: float = 1.0, scale_b: float = 1.0, out: Optional[torch.Tensor] = None,
-                     stream=None) -> torch.Tensor:
+                     err_flag=None, stream=None) -> torch.Tensor:
     """mla_group_wo on FP4 weights -> (B,Q,D), or (B,Q,G*R) without ``wo_b``.
 
     x (B,H,Q,512) bf16; wo_a (G,R,H/G,288) entries of (G, R, (H/G)*512) weights;
     wo_b (D,G*R/512,288). z is rounded to bf16 between the factors, as there.
     """
-    _need(x.dim() == 4 and x.shape[-1] == FP4_BLOCK and x.stride(-1) == 1, "mla_fp4_group_wo: x must be (B, H, Q, 512)")
+    if x.dim() != 4 or x.shape[-1] != FP4_BLOCK or wo_a.dim() != 4:
+        raise MlaError("mla_fp4_group_wo: x must be (B, H, Q, 512) and wo_a (G, R, H/G, 288)")
     B, H, Q, _ = x.shape
-    _need(wo_a.dim() == 4 and wo_a.shape[0] * wo_a.shape[2] == H, "mla_fp4_group_wo: wo_a must be (G, R, H/G, 288)")
     G, R, per, _ = wo_a.shape
-    if x.data_ptr() % 16 or any(s % 8 for s in x.stride()[:3]):
+    if G * per != H:
+        raise MlaError("mla_fp4_group_wo: wo_a must be (G, R, H/G, 288)")
+    sb, sh, sq, one = x.stride()
+    if one != 1 or sb % 8 or sh % 8 or sq % 8 or x.data_ptr() % 16:
         x = x.contiguous()
-    z = out if wo_b is None and out is not None else torch.empty((B, Q, G * R), dtype=torch.bfloat16, device=x.device)
-    _need(tuple(z.shape) == (B, Q, G * R), "mla_fp4_group_wo: out has another shape")
-    a = Fp4LinearArgs()
-    a.B, a.Q, a.G, a.N, a.K = B, Q, G, R, per * FP4_BLOCK
-    a.x_batch_stride, a.x_block_stride, a.x_token_stride = x.stride()[:3]
-    a.x_group_stride = per * x.stride(1)
-    _fp4_linear(x, a, wo_a, scale_a, z, stream)
-    return z if wo_b is None else mla_fp4_linear(z, wo_b, scale_b, out=out, stream=stream)
+        sb, sh, sq, one = x.stride()
+    z = out if wo_b is None else None
+    if z is None:
+        z = torch.empty((B, Q, G * R), dtype=torch.bfloat16, device=x.device)
+    elif tuple(z.shape) != (B, Q, G * R):
+        raise MlaError("mla_fp4_group_wo: out has another shape")
+    _fp4_linear(x, wo_a, (B, Q, G, R, per * FP4_BLOCK), (sb, sq, per * sh, sh), scale_a, z, err_flag, stream)
+    if wo_b is None:
+        return z
+    return mla_fp4_linear(z, wo_b, scale_b, out=out, err_flag=err_flag, stream=stream)
