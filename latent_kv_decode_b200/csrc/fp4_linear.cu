@@ -3,11 +3,15 @@
 // The weights are the bytes: 0.5625 per element, read once per 64 tokens. What
 // it takes to stream them is to turn 4-bit codes into tensor-core operands as
 // fast as HBM delivers them (about 40 weights per clock and SM), so the operand
-// type is float16: every E2M1 x E4M3 product has 6 significant bits between
-// 2^-10 and 2688 and is exact there, and one conversion and one multiply make
-// two of them. The activations follow: a first kernel scales each token's row
-// by a power of two that brings its largest finite magnitude to [2^14, 2^15) and
-// stores it as float16. bf16 values keep their 8 bits down to 2^-29 of that
+// type is float16: a code's magnitude bits moved to the bottom of the exponent
+// and the top of the mantissa are its value times 2^-14 (subnormals included),
+// so two shifts, two logic operations and one multiply by scale * 2^7 make two
+// weights times 2^-7. That is exact: E2M1 x E4M3 products are multiples of 2^-10
+// with 6 significant bits, at most 2688. (The conversion instruction runs on
+// the pipe of the special functions, 16 lanes a clock: 50 us for the 66 MB of
+// the 16384 x 7168 case, where that pipe was 71% busy.) The activations follow: a
+// first kernel scales each token's row by a power of two that brings its
+// largest finite magnitude to [2^14, 2^15) and stores it as float16. bf16 values keep their 8 bits down to 2^-29 of that
 // magnitude, and below it the error is under 2^-40 of it, far below float32's
 // accumulation. The epilogue takes the power of two out again.
 //
@@ -19,7 +23,6 @@
 //                 issues the MMAs (M = 128, N = tokens) into TMEM. The S partial
 //                 sums meet through distributed shared memory in a fixed order.
 #include <cuda_fp16.h>
-#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -106,12 +109,18 @@ __global__ void __launch_bounds__(256) x_to_f16(const mla_fp4_linear_args a, __h
   const float f1 = scalbnf(1.f, -e / 2), f2 = scalbnf(1.f, -e - (-e / 2));
   __half* dst = xs + ((int64_t)g * T + t) * a.K;
   auto store = [&](int k, const uint4& u) {
+    // channels in the order 0 4 1 5 2 6 3 7 that the weights decode to
     const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(wd[i] << 16) * f1 * f2;
+      f[2 * i + 1] = __uint_as_float(wd[i] & 0xffff0000u) * f1 * f2;
+    }
     uint32_t r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __half2 h = __floats2half2_rn(__uint_as_float(wd[i] << 16) * f1 * f2,
-                                          __uint_as_float(wd[i] & 0xffff0000u) * f1 * f2);
+      const __half2 h = __floats2half2_rn(f[i], f[i + 4]);
       r[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
     *reinterpret_cast<uint4*>(dst + k) = make_uint4(r[0], r[1], r[2], r[3]);
@@ -160,10 +169,13 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
 
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
-// two codes of a byte times the group's scale
-__device__ __forceinline__ uint32_t decode2(uint32_t byte, __half2 s) {
-  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1);
-  return half2_bits(__hmul2(__half2(h), s));
+// codes i and i + 4 of a word times 2^-14 s
+template <int i>
+__device__ __forceinline__ uint32_t decode2(uint32_t w, __half2 s) {
+  const uint32_t mag = i < 3 ? w << (9 - 4 * (i < 3 ? i : 0)) : w >> 3;   // bits 4i .. 4i+2 to 9 .. 11
+  const uint32_t sgn = w << (12 - 4 * i);                                  // bit 4i+3 to 15
+  const uint32_t u = (mag & 0x0e000e00u) | (sgn & 0x80008000u);
+  return half2_bits(__hmul2(*reinterpret_cast<const __half2*>(&u), s));
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -254,7 +266,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_co
         uint8_t* A = smem + stage * stage_bytes;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const __half2 s2 = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)sc[u][h], __NV_E4M3));
+          const __half2 s2 = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)sc[u][h], __NV_E4M3)),
+                                     __float2half2_rn(128.f));
           const uint32_t wd[4] = {q[u][h].x, q[u][h].y, q[u][h].z, q[u][h].w};
 #pragma unroll
           for (int ii = 0; ii < 4; ++ii) {
@@ -262,8 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_co
             const uint32_t x = flip ? wd[ii ^ 2] : wd[ii];
             const int i = flip ? ii ^ 2 : ii;
             const __half2 s = i < 2 ? __low2half2(s2) : __high2half2(s2);
-            const uint4 v = make_uint4(decode2(x & 255u, s), decode2((x >> 8) & 255u, s), decode2((x >> 16) & 255u, s),
-                                       decode2(x >> 24, s));
+            const uint4 v = make_uint4(decode2<0>(x, s), decode2<1>(x, s), decode2<2>(x, s), decode2<3>(x, s));
             *reinterpret_cast<uint4*>(A + dst[h] + 16 * ((c16 + i) ^ sw)) = v;
           }
         }
@@ -322,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_co
         ph ^= 1;
       }
     }
-    if (ok) commit_one(el, bar(B_DONE));
+    if (ok && nc > 0) commit_one(el, bar(B_DONE));
   }
   if (!ok) *reinterpret_cast<volatile int*>(&failed) = 1;
   __syncthreads();
@@ -332,13 +344,18 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_co
   // this CTA's sums as [token][row] in shared memory; then rank r sums the
   // cluster's partial results of tokens r, r + S, ... in rank order
   float* part = reinterpret_cast<float*>(smem);
-  if (!failed && !mbar_wait(bar(B_DONE), 0)) *reinterpret_cast<volatile int*>(&failed) = 1;
+  if (nc > 0 && !failed && !mbar_wait(bar(B_DONE), 0)) *reinterpret_cast<volatile int*>(&failed) = 1;
   tc_fence_after();
   if (warp < 4) {
     for (int c = 0; c < P.tok_pad; c += 16) {
       uint32_t v[16];
-      tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + (uint32_t)c, v);
-      tmem_wait_ld();
+      if (nc > 0) {
+        tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + (uint32_t)c, v);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0u;
+      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) part[(c + i) * kRowsM + 32 * warp + lane] = __uint_as_float(v[i]);
     }
@@ -356,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_co
       for (uint32_t k = 0; k < S; ++k) sum += ld_cluster_f32(map_to_rank(mine + 4u * (uint32_t)(i * kRowsM + r), k));
       if (n0 + r < P.N)
         P.out[(int64_t)(t0 + i) * P.G * P.N + (int64_t)g * P.N + n0 + r] = __float2bfloat16_rn(
-            (float)ldexp((double)sum * (double)P.scale, P.exps[g * P.T + t0 + i]));
+            (float)ldexp((double)sum * (double)P.scale, P.exps[g * P.T + t0 + i] + 7));
     }
   }
   cluster_sync();                            // the peers have read this CTA's sums
@@ -430,8 +447,8 @@ cudaError_t launch_fp4_linear(const mla_fp4_linear_args* a, void* ws, int sms, c
 
   // K over as many CTAs as two per SM hold, each with at least one chunk
   const int64_t clusters = (int64_t)a->G * P.tiles * ((T + kTokMax - 1) / kTokMax);
-  int S = 1;
-  while (S < 8 && clusters * S * 2 <= 2 * sms && S * 2 <= a->K / kChunkK) S *= 2;
+  const int64_t fit = 2 * sms / clusters;
+  const int S = (int)(fit < 1 ? 1 : fit > 8 ? 8 : fit);   // K holds 4 chunks or more; a rank may get none
   const size_t smem = (size_t)P.stages * (kABytes + P.tok_pad * kChunkK * 2) + 1024;
   e = cudaFuncSetAttribute(fp4_linear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
