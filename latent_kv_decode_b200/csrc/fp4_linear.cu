@@ -17,11 +17,14 @@
 //
 //   x_to_f16      one CTA per (token, group): largest magnitude, then the row.
 //   fp4_linear    one cluster of S CTAs per 128 output rows and 64 tokens, each a
-//                 range of K in chunks of 128. 8 warps load codes and scales from
-//                 global memory kAhead chunks ahead, convert, and write the K-major
-//                 128-byte-swizzled A tile; TMA brings the tokens' B tile; one warp
-//                 issues the MMAs (M = 128, N = tokens) into TMEM. The S partial
-//                 sums meet through distributed shared memory in a fixed order.
+//                 range of K in entries of 512 channels. TMA brings the rows'
+//                 288-byte entries, whole, into a ring (read in 64-byte pieces by
+//                 the converting threads themselves the same bytes took 45 us
+//                 instead of WIDE us); 16 warps turn 128 channels at a time into
+//                 the K-major 128-byte-swizzled A tile; TMA brings the tokens' B
+//                 tile; one warp issues the MMAs (M = 128, N = tokens) into TMEM.
+//                 The S partial sums meet through distributed shared memory in
+//                 rank order.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
@@ -39,24 +42,34 @@ using namespace sm100;
 
 constexpr int kRowsM = 128;                  // output rows per cluster
 constexpr int kTokMax = 64;                  // tokens per cluster
-constexpr int kChunkK = 128;                 // channels per stage: two 64-wide swizzled blocks
-constexpr int kABytes = kRowsM * kChunkK * 2;
-constexpr int kConv = 256;                   // converting threads
-constexpr int kThreads = kConv + 64;         // + TMA warp + MMA warp
-constexpr int kAhead = 3;                    // chunks a converting thread has in flight
-constexpr int kMaxStages = 3;
+constexpr int kChunkK = 128;                 // channels per A stage (64 columns) and token tile (two swizzled blocks)
+constexpr int kPer = kCkv / kChunkK;         // A stages: one entry
+constexpr int kRawBytes = kRowsM * kFp4EntryBytes;
+constexpr int kRaw = 4, kX = 4;              // stages: entries, token tiles
+constexpr uint32_t kColA = 64;               // TMEM columns: sums at 0, A stages from 64
+constexpr uint32_t kTmemCols = 512;
+constexpr int kConv = 512;                   // converting threads: 128 rows x 4 x 32 channels
+constexpr int kThreads = kConv + 64;         // + load warp + MMA warp
 
-enum : int { B_AF = 0, B_XF = kMaxStages, B_EMPTY = 2 * kMaxStages, B_DONE = 3 * kMaxStages, B_COUNT = B_DONE + 1 };
+enum : int {
+  B_RF = 0,                // [kRaw] entries landed
+  B_RE = B_RF + kRaw,      // [kRaw] entries converted (one arrival per converting warp)
+  B_AF = B_RE + kRaw,      // [kPer] A stage written (one arrival per converting warp)
+  B_AE = B_AF + kPer,      // [kPer] MMAs over the A stage done
+  B_XF = B_AE + kPer,        // [kX] token tile landed
+  B_XE = B_XF + kX,        // [kX] MMAs over the token tile done
+  B_DONE = B_XE + kX,
+  B_COUNT
+};
 
 struct alignas(64) LinearParams {
   CUtensorMap tm_x;                          // scaled activations (K, T, G) float16, box 64 x tokens
-  const uint8_t* w;
+  CUtensorMap tm_w;                          // entries as (words of a row, N, G), box 72 words x 128 rows
   const int* exps;                           // (G, T): token t's row holds x 2^-exps
   __nv_bfloat16* out;
   int T, G, N, K;
   int tok_pad;                               // tokens per cluster, a multiple of 16
   int tiles;                                 // 128-row tiles per group
-  int stages;
   float scale;
   int32_t* err;
 };
@@ -142,15 +155,15 @@ __device__ __forceinline__ uint32_t elect_one() {
   return e;
 }
 
-// One MMA, or a commit, by the elected lane (e != 0) of a converged warp.
-__device__ __forceinline__ void mma_one(uint32_t e, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+// One MMA with A in TMEM, or a commit, by the elected lane (e != 0) of a converged warp.
+__device__ __forceinline__ void mma_one(uint32_t e, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                         uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(e)
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(e)
       : "memory");
 }
 __device__ __forceinline__ void commit_one(uint32_t e, uint32_t bar) {
@@ -178,13 +191,29 @@ __device__ __forceinline__ uint32_t decode2(uint32_t w, __half2 s) {
   return half2_bits(__hmul2(*reinterpret_cast<const __half2*>(&u), s));
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
-__global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_constant__ LinearParams P) {
+// A ring position: the stage and the parity of its current pass.
+template <int kStages>
+struct Ring {
+  int stage = 0;
+  uint32_t par = 0;
+  __device__ __forceinline__ void step() {
+    if (++stage == kStages) {
+      stage = 0;
+      par ^= 1;
+    }
+  }
+};
+
+__global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_constant__ LinearParams P) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ alignas(8) uint64_t bars[B_COUNT];
   __shared__ uint32_t tmem_ptr;
@@ -194,7 +223,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_co
   uint8_t* smem = smem_raw + (sb0 - raw);
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return smem_u32(bars + i); };
-  const int stage_bytes = kABytes + P.tok_pad * kChunkK * 2;
+  const int x_bytes = P.tok_pad * kChunkK * 2;
+  const int off_raw = 0, off_x = kRaw * kRawBytes;
 
   uint32_t S;
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(S));
@@ -202,21 +232,23 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_co
   const int tile = blockIdx.x / S;           // (group, 128 rows)
   const int g = tile / P.tiles, n0 = (tile - g * P.tiles) * kRowsM;
   const int t0 = blockIdx.y * kTokMax;
-  const int chunks = P.K / kChunkK;
-  const int c_begin = (int)((int64_t)chunks * rank / S), nc = (int)((int64_t)chunks * (rank + 1) / S) - c_begin;
+  const int entries = P.K / kCkv;
+  const int e_begin = (int)((int64_t)entries * rank / S), ne = (int)((int64_t)entries * (rank + 1) / S) - e_begin;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(bar(B_AF + i), kConv / 32);
-      mbar_init(bar(B_XF + i), 1);
-      mbar_init(bar(B_EMPTY + i), 1);
-    }
-    mbar_init(bar(B_DONE), 1);
+  auto load_entry = [&](int i, int stage) {
+    mbar_arrive_expect_tx(bar(B_RF + stage), kRawBytes);
+    tma_load_3d(sb0 + off_raw + stage * kRawBytes, &P.tm_w, bar(B_RF + stage), (e_begin + i) * (kFp4EntryBytes / 4), n0, g);
+  };
+  if (threadIdx.x == kConv) {                // the load warp's first lane
+    for (int i = 0; i < B_COUNT; ++i)
+      mbar_init(bar(i), i >= B_RE && i < B_AE ? kConv / 32 : 1);
     failed = 0;
     fence_mbar_init();
+    for (int i = 0; i < kRaw && i < ne; ++i) load_entry(i, i);   // weights do not wait for the first kernel
   }
-  if (warp == kConv / 32) {
-    tmem_alloc(smem_u32(&tmem_ptr), 64);
+  __syncwarp();
+  if (warp == kConv / 32 + 1) {
+    tmem_alloc(smem_u32(&tmem_ptr), kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -227,85 +259,69 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_co
 
   if (warp < kConv / 32) {
     // ------------------------------------------------------------------ converting warps
-    // lane: row 8 warp + lane / 4 (and 64 further on), channels 32 (lane % 4) .. + 31
-    // of the chunk: 16 bytes of codes and two scales
-    const int seg = lane & 3;
-    const uint8_t* src[2];
-    uint32_t dst[2];
+    // Warp w decodes rows 32 (w % 4) + lane, channels 32 (w / 4) .. + 31 of each
+    // 128: 16 bytes of codes and two scales become 16 packed pairs, which are
+    // 16 columns of the row's TMEM lane.
+    const int r = 32 * (warp & 3) + lane, seg = warp >> 2;
+    const uint32_t a_tmem = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColA + 16u * (uint32_t)seg;
+    Ring<kRaw> rr;
+    for (int e = 0; e < ne && ok; ++e) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(B_RF + rr.stage), rr.par));
+      if (!ok) break;
+      const uint8_t* src = smem + off_raw + rr.stage * kRawBytes + r * kFp4EntryBytes;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = 64 * h + 8 * warp + (lane >> 2);
-      const int64_t row = (int64_t)g * P.N + min(n0 + r, P.N - 1);       // rows behind the last repeat it
-      src[h] = P.w + row * (P.K / kCkv) * kFp4EntryBytes;
-      dst[h] = (uint32_t)((seg >> 1) * (kRowsM * 128) + r * 128);
-    }
-    const int sw = (8 * warp + (lane >> 2)) & 7, c16 = 4 * (seg & 1), flip = (seg >> 1) << 1;
-    uint4 q[kAhead][2];
-    uint32_t sc[kAhead][2];
-    auto fetch = [&](int c, uint4 (&qq)[2], uint32_t (&ss)[2]) {
-      if (c >= nc) return;
-      const int k = (c_begin + c) * kChunkK;
-      const int64_t e = (int64_t)(k >> 9) * kFp4EntryBytes;
-      const int in = k & 511;
+      for (int c = 0; c < kPer; ++c) {
+        const uint4 q = *reinterpret_cast<const uint4*>(src + 64 * c + 16 * seg);
+        const uint32_t sc = *reinterpret_cast<const unsigned short*>(src + kCkv / 2 + 8 * c + 2 * seg);
+        const __half2 s2 = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)sc, __NV_E4M3)),
+                                   __float2half2_rn(128.f));
+        const uint32_t wd[4] = {q.x, q.y, q.z, q.w};
+        uint32_t v[16];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint8_t* p = src[h] + e;
-        qq[h] = __ldcs(reinterpret_cast<const uint4*>(p + in / 2 + 16 * seg));
-        ss[h] = __ldcs(reinterpret_cast<const unsigned short*>(p + kCkv / 2 + in / 16 + 2 * seg));
-      }
-    };
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) fetch(u, q[u], sc[u]);
-    int stage = 0, ph = 1;                   // the ring starts empty
-    for (int c0 = 0; c0 < nc && ok; c0 += kAhead) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (c0 + u >= nc || !ok) break;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(B_EMPTY + stage), ph));
+        for (int i = 0; i < 4; ++i) {
+          const __half2 s = i < 2 ? __low2half2(s2) : __high2half2(s2);
+          v[4 * i] = decode2<0>(wd[i], s);
+          v[4 * i + 1] = decode2<1>(wd[i], s);
+          v[4 * i + 2] = decode2<2>(wd[i], s);
+          v[4 * i + 3] = decode2<3>(wd[i], s);
+        }
+        if (c == kPer - 1) {                 // the entry is in registers
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_RE + rr.stage));
+        }
+        if (e > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_AE + c), (uint32_t)(e - 1) & 1u));
         if (!ok) break;
-        uint8_t* A = smem + stage * stage_bytes;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const __half2 s2 = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)sc[u][h], __NV_E4M3)),
-                                     __float2half2_rn(128.f));
-          const uint32_t wd[4] = {q[u][h].x, q[u][h].y, q[u][h].z, q[u][h].w};
-#pragma unroll
-          for (int ii = 0; ii < 4; ++ii) {
-            // the two 64-channel blocks in another order, so that eight lanes hit all banks
-            const uint32_t x = flip ? wd[ii ^ 2] : wd[ii];
-            const int i = flip ? ii ^ 2 : ii;
-            const __half2 s = i < 2 ? __low2half2(s2) : __high2half2(s2);
-            const uint4 v = make_uint4(decode2<0>(x, s), decode2<1>(x, s), decode2<2>(x, s), decode2<3>(x, s));
-            *reinterpret_cast<uint4*>(A + dst[h] + 16 * ((c16 + i) ^ sw)) = v;
-          }
-        }
-        fence_proxy_async_smem();
+        tc_fence_after();
+        tmem_st16(a_tmem + (uint32_t)(c * kChunkK / 2), v);
+        tmem_wait_st();
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_AF + stage));
-        fetch(c0 + u + kAhead, q[u], sc[u]);
-        if (++stage == P.stages) {
-          stage = 0;
-          ph ^= 1;
-        }
+        if (lane == 0) mbar_arrive(bar(B_AF + c));
       }
+      rr.step();
     }
   } else if (warp == kConv / 32) {
-    // ------------------------------------------------------------------ token loads
+    // ------------------------------------------------------------------ loads
     pdl_wait();                              // the first kernel's rows
     if (lane == 0) {
-      tma_prefetch_desc(&P.tm_x);
-      int stage = 0, ph = 1;
-      for (int c = 0; c < nc; ++c) {
-        ok = mbar_wait(bar(B_EMPTY + stage), ph);
+      Ring<kRaw> rr;
+      Ring<kX> rx;
+      for (int c = 0; c < ne * kPer && ok; ++c) {
+        ok = mbar_wait(bar(B_XE + rx.stage), rx.par ^ 1);
         if (!ok) break;
-        mbar_arrive_expect_tx(bar(B_XF + stage), (uint32_t)(P.tok_pad * kChunkK * 2));
-        const uint32_t xb = sb0 + stage * stage_bytes + kABytes;
-        const int k = (c_begin + c) * kChunkK;
-        tma_load_3d(xb, &P.tm_x, bar(B_XF + stage), k, t0, g);
-        tma_load_3d(xb + P.tok_pad * 128, &P.tm_x, bar(B_XF + stage), k + 64, t0, g);
-        if (++stage == P.stages) {
-          stage = 0;
-          ph ^= 1;
+        mbar_arrive_expect_tx(bar(B_XF + rx.stage), (uint32_t)x_bytes);
+        const uint32_t xb = sb0 + off_x + rx.stage * x_bytes;
+        const int k = e_begin * kCkv + c * kChunkK;
+        tma_load_3d(xb, &P.tm_x, bar(B_XF + rx.stage), k, t0, g);
+        tma_load_3d(xb + P.tok_pad * 128, &P.tm_x, bar(B_XF + rx.stage), k + 64, t0, g);
+        rx.step();
+        // entry c / kPer + kRaw into the stage that entry c / kPer leaves
+        if (c % kPer == kPer - 1) {
+          if (c / kPer + kRaw < ne) {
+            ok = mbar_wait(bar(B_RE + rr.stage), rr.par);
+            if (ok) load_entry(c / kPer + kRaw, rr.stage);
+          }
+          rr.step();
         }
       }
     }
@@ -314,70 +330,80 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_co
     // ------------------------------------------------------------------ MMA issue
     const uint32_t el = elect_one();
     const uint32_t idesc = idesc_f16_f32(kRowsM, P.tok_pad);
-    int stage = 0, ph = 0;
-    for (int c = 0; c < nc; ++c) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(B_XF + stage), ph) && mbar_wait(bar(B_AF + stage), ph));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t base = sb0 + stage * stage_bytes;
+    Ring<kX> rx;
+    for (int e = 0; e < ne && ok; ++e) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const uint64_t ad = smem_desc(base + b * (kRowsM * 128), 16, 1024, kSwizzle128B);
-        const uint64_t bd = smem_desc(base + kABytes + b * P.tok_pad * 128, 16, 1024, kSwizzle128B);
+      for (int c = 0; c < kPer; ++c) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(B_XF + rx.stage), rx.par) && mbar_wait(bar(B_AF + c), (uint32_t)e & 1u));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t xb = sb0 + off_x + rx.stage * x_bytes;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_one(el, tmem, desc_advance(ad, 32 * k), desc_advance(bd, 32 * k), idesc, c > 0 || b > 0 || k > 0);
-      }
-      commit_one(el, bar(B_EMPTY + stage));
-      if (++stage == P.stages) {
-        stage = 0;
-        ph ^= 1;
+        for (int b = 0; b < 2; ++b) {
+          const uint64_t bd = smem_desc(xb + b * P.tok_pad * 128, 16, 1024, kSwizzle128B);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_one(el, tmem, tmem + kColA + (uint32_t)(c * kChunkK / 2 + b * 32 + k * 8), desc_advance(bd, 32 * k),
+                    idesc, e > 0 || c > 0 || b > 0 || k > 0);
+        }
+        commit_one(el, bar(B_AE + c));
+        commit_one(el, bar(B_XE + rx.stage));
+        rx.step();
       }
     }
-    if (ok && nc > 0) commit_one(el, bar(B_DONE));
+    if (ok && ne > 0) commit_one(el, bar(B_DONE));
   }
   if (!ok) *reinterpret_cast<volatile int*>(&failed) = 1;
   __syncthreads();
   pdl_wait();                                // exps, for every thread
 
   // ---------------------------------------------------------------- epilogue
-  // this CTA's sums as [token][row] in shared memory; then rank r sums the
-  // cluster's partial results of tokens r, r + S, ... in rank order
+  // this CTA's sums as [token][row] in shared memory (its tiles are used up);
+  // rank r sums the cluster's partial results of tokens r, r + S, ... in rank order
   float* part = reinterpret_cast<float*>(smem);
-  if (nc > 0 && !failed && !mbar_wait(bar(B_DONE), 0)) *reinterpret_cast<volatile int*>(&failed) = 1;
+  if (ne > 0 && !failed && !mbar_wait(bar(B_DONE), 0)) *reinterpret_cast<volatile int*>(&failed) = 1;
   tc_fence_after();
-  if (warp < 4) {
-    for (int c = 0; c < P.tok_pad; c += 16) {
-      uint32_t v[16];
-      if (nc > 0) {
-        tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + (uint32_t)c, v);
-        tmem_wait_ld();
-      } else {
+  for (int c = 16 * (warp >> 2); c < P.tok_pad && warp < kConv / 32; c += 64) {
+    uint32_t v[16];
+    if (ne > 0) {
+      tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)c, v);
+      tmem_wait_ld();
+    } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0u;
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) part[(c + i) * kRowsM + 32 * warp + lane] = __uint_as_float(v[i]);
+      for (int i = 0; i < 16; ++i) v[i] = 0u;
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) part[(c + i) * kRowsM + 32 * (warp & 3) + lane] = __uint_as_float(v[i]);
   }
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && failed && P.err) atomicOr(P.err, MLA_DEVICE_ERR_TIMEOUT);
   cluster_sync();
-  if (warp < kConv / 32) {
-    const int r = threadIdx.x & 127;
-    const uint32_t mine = smem_u32(part);
-    const int nt = min(P.tok_pad, P.T - t0);
-    for (int i = (int)(threadIdx.x >> 7) * (int)S + (int)rank; i < nt; i += 2 * (int)S) {
-      float sum = 0.f;
-      for (uint32_t k = 0; k < S; ++k) sum += ld_cluster_f32(map_to_rank(mine + 4u * (uint32_t)(i * kRowsM + r), k));
-      if (n0 + r < P.N)
-        P.out[(int64_t)(t0 + i) * P.G * P.N + (int64_t)g * P.N + n0 + r] = __float2bfloat16_rn(
-            (float)ldexp((double)sum * (double)P.scale, P.exps[g * P.T + t0 + i] + 7));
+  const int nt = min(P.tok_pad, P.T - t0);
+  for (int i = warp * (int)S + (int)rank; i < nt && warp < kConv / 32; i += kConv / 32 * (int)S) {
+    const uint32_t mine = smem_u32(part + i * kRowsM + 4 * lane);
+    float4 v[8];
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k)
+      if (k < S) v[k] = ld_cluster_f32x4(map_to_rank(mine, k));
+    float4 sum = v[0];
+#pragma unroll
+    for (uint32_t k = 1; k < 8; ++k)
+      if (k < S) sum = make_float4(sum.x + v[k].x, sum.y + v[k].y, sum.z + v[k].z, sum.w + v[k].w);
+    const double f = ldexp((double)P.scale, P.exps[g * P.T + t0 + i] + 7);
+    const float y[4] = {(float)(sum.x * f), (float)(sum.y * f), (float)(sum.z * f), (float)(sum.w * f)};
+    const int n = n0 + 4 * lane;
+    __nv_bfloat16* out = P.out + (int64_t)(t0 + i) * P.G * P.N + (int64_t)g * P.N + n;
+    if (n + 3 < P.N && (reinterpret_cast<uintptr_t>(out) & 7u) == 0) {
+      *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (n + k < P.N) out[k] = __float2bfloat16_rn(y[k]);
     }
   }
   cluster_sync();                            // the peers have read this CTA's sums
-  if (warp == kConv / 32) tmem_dealloc(tmem, 64);
+  if (warp == kConv / 32 + 1) tmem_dealloc(tmem, kTmemCols);
 }
 
 // ---------------------------------------------------------------------------
@@ -412,7 +438,6 @@ cudaError_t launch_fp4_linear(const mla_fp4_linear_args* a, void* ws, int sms, c
   const int T = a->B * a->Q;
   __half* xs = reinterpret_cast<__half*>(ws);
   int* exps = reinterpret_cast<int*>(reinterpret_cast<char*>(ws) + xs_bytes(a));
-  P.w = reinterpret_cast<const uint8_t*>(a->w);
   P.exps = exps;
   P.out = reinterpret_cast<__nv_bfloat16*>(a->out);
   P.T = T;
@@ -423,13 +448,21 @@ cudaError_t launch_fp4_linear(const mla_fp4_linear_args* a, void* ws, int sms, c
   P.err = a->err_flag;
   P.tok_pad = T >= kTokMax ? kTokMax : (T + 15) / 16 * 16;
   P.tiles = (a->N + kRowsM - 1) / kRowsM;
-  P.stages = P.tok_pad <= 16 ? 3 : 2;        // two CTAs per SM
   {
     const cuuint64_t d[3] = {(cuuint64_t)a->K, (cuuint64_t)T, (cuuint64_t)a->G};
     const cuuint64_t s[2] = {(cuuint64_t)a->K * 2, (cuuint64_t)a->K * 2 * T};
     const cuuint32_t bx[3] = {64, (cuuint32_t)P.tok_pad, 1}, el[3] = {1, 1, 1};
     if (encode_fn()(&P.tm_x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, xs, d, s, bx, el, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  {
+    const cuuint64_t pitch = (cuuint64_t)(a->K / kCkv) * kFp4EntryBytes;
+    const cuuint64_t d[3] = {pitch / 4, (cuuint64_t)a->N, (cuuint64_t)a->G}, s[2] = {pitch, pitch * a->N};
+    const cuuint32_t bx[3] = {kFp4EntryBytes / 4, kRowsM, 1}, el[3] = {1, 1, 1};
+    if (encode_fn()(&P.tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(a->w), d, s, bx, el,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
@@ -445,14 +478,16 @@ cudaError_t launch_fp4_linear(const mla_fp4_linear_args* a, void* ws, int sms, c
   cudaError_t e = cudaLaunchKernelEx(&cfg, x_to_f16, *a, xs, exps);
   if (e != cudaSuccess) return e;
 
-  // K over as many CTAs as two per SM hold, each with at least one chunk
+  // K over as many CTAs as there are SMs (a CTA's rings fill one), in entries
   const int64_t clusters = (int64_t)a->G * P.tiles * ((T + kTokMax - 1) / kTokMax);
-  const int64_t fit = 2 * sms / clusters;
-  const int S = (int)(fit < 1 ? 1 : fit > 8 ? 8 : fit);   // K holds 4 chunks or more; a rank may get none
-  const size_t smem = (size_t)P.stages * (kABytes + P.tok_pad * kChunkK * 2) + 1024;
+  int64_t S = sms / clusters;
+  if (S > a->K / kCkv) S = a->K / kCkv;
+  if (S > 8) S = 8;
+  if (S < 1) S = 1;
+  const size_t smem = (size_t)kRaw * kRawBytes + (size_t)kX * P.tok_pad * kChunkK * 2 + 1024;
   e = cudaFuncSetAttribute(fp4_linear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)(a->G * P.tiles * S), (unsigned)((T + kTokMax - 1) / kTokMax));
+  cfg.gridDim = dim3((unsigned)((int64_t)a->G * P.tiles * S), (unsigned)((T + kTokMax - 1) / kTokMax));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   attr[1].id = cudaLaunchAttributeClusterDimension;
