@@ -17,14 +17,13 @@
 //
 //   x_to_f16      one CTA per (token, group): largest magnitude, then the row.
 //   fp4_linear    one cluster of S CTAs per 128 output rows and 64 tokens, each a
-//                 range of K in entries of 512 channels. TMA brings the rows'
-//                 288-byte entries, whole, into a ring (read in 64-byte pieces by
-//                 the converting threads themselves the same bytes took 45 us
-//                 instead of WIDE us); 16 warps turn 128 channels at a time into
-//                 the K-major 128-byte-swizzled A tile; TMA brings the tokens' B
-//                 tile; one warp issues the MMAs (M = 128, N = tokens) into TMEM.
-//                 The S partial sums meet through distributed shared memory in
-//                 rank order.
+//                 range of K in entries of 512 channels, two CTAs per SM. TMA
+//                 brings the rows' 288-byte entries into a ring; 8 warps decode
+//                 them, 128 channels at a time, straight into the A operand in
+//                 tensor memory (through a shared-memory A tile its writes and
+//                 reads were the bound); TMA brings the tokens' B tile; one warp
+//                 issues the MMAs (M = 128, N = tokens). The S partial sums meet
+//                 through distributed shared memory in rank order.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
@@ -43,20 +42,20 @@ using namespace sm100;
 constexpr int kRowsM = 128;                  // output rows per cluster
 constexpr int kTokMax = 64;                  // tokens per cluster
 constexpr int kChunkK = 128;                 // channels per A stage (64 columns) and token tile (two swizzled blocks)
-constexpr int kPer = kCkv / kChunkK;         // A stages: one entry
+constexpr int kPer = kCkv / kChunkK;         // chunks per entry
 constexpr int kRawBytes = kRowsM * kFp4EntryBytes;
-constexpr int kRaw = 4, kX = 4;              // stages: entries, token tiles
+constexpr int kRaw = 2, kA = 3, kX = 2;      // stages: entries, A chunks, token tiles; two CTAs per SM
 constexpr uint32_t kColA = 64;               // TMEM columns: sums at 0, A stages from 64
-constexpr uint32_t kTmemCols = 512;
-constexpr int kConv = 512;                   // converting threads: 128 rows x 4 x 32 channels
+constexpr uint32_t kTmemCols = 256;
+constexpr int kConv = 256;                   // converting threads: two chunks of 128 rows at a time
 constexpr int kThreads = kConv + 64;         // + load warp + MMA warp
 
 enum : int {
   B_RF = 0,                // [kRaw] entries landed
   B_RE = B_RF + kRaw,      // [kRaw] entries converted (one arrival per converting warp)
-  B_AF = B_RE + kRaw,      // [kPer] A stage written (one arrival per converting warp)
-  B_AE = B_AF + kPer,      // [kPer] MMAs over the A stage done
-  B_XF = B_AE + kPer,        // [kX] token tile landed
+  B_AF = B_RE + kRaw,      // [kA] A stage written (one arrival per warp of four)
+  B_AE = B_AF + kA,        // [kA] MMAs over the A stage done
+  B_XF = B_AE + kA,        // [kX] token tile landed
   B_XE = B_XF + kX,        // [kX] MMAs over the token tile done
   B_DONE = B_XE + kX,
   B_COUNT
@@ -182,13 +181,31 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
 
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
-// codes i and i + 4 of a word times 2^-14 s
-template <int i>
-__device__ __forceinline__ uint32_t decode2(uint32_t w, __half2 s) {
-  const uint32_t mag = i < 3 ? w << (9 - 4 * (i < 3 ? i : 0)) : w >> 3;   // bits 4i .. 4i+2 to 9 .. 11
-  const uint32_t sgn = w << (12 - 4 * i);                                  // bit 4i+3 to 15
-  const uint32_t u = (mag & 0x0e000e00u) | (sgn & 0x80008000u);
-  return half2_bits(__hmul2(*reinterpret_cast<const __half2*>(&u), s));
+// Powers of two in registers the compiler cannot see through: a left shift
+// written as a multiply by one of them runs on the multiplier's pipe, beside the
+// logic operations, which keep the other integer pipe busy by themselves.
+struct Shifts {
+  uint32_t p1, p4, p5, p8, p9, p12;
+  __device__ __forceinline__ Shifts() {
+    asm volatile("mov.u32 %0, 2;" : "=r"(p1));
+    asm volatile("mov.u32 %0, 16;" : "=r"(p4));
+    asm volatile("mov.u32 %0, 32;" : "=r"(p5));
+    asm volatile("mov.u32 %0, 256;" : "=r"(p8));
+    asm volatile("mov.u32 %0, 512;" : "=r"(p9));
+    asm volatile("mov.u32 %0, 4096;" : "=r"(p12));
+  }
+};
+
+// The eight codes of a word times 2^-14 s: codes i and i + 4 in v[i]. Bits 4i ..
+// 4i+2 (of each half) go to 9 .. 11, bit 4i+3 to 15.
+__device__ __forceinline__ void decode8(uint32_t w, __half2 s, const Shifts& p, uint32_t* v) {
+  const uint32_t mag[4] = {w * p.p9, w * p.p5, w * p.p1, w >> 3};
+  const uint32_t sgn[4] = {w * p.p12, w * p.p8, w * p.p4, w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = (mag[i] & 0x0e000e00u) | (sgn[i] & 0x80008000u);
+    v[i] = half2_bits(__hmul2(*reinterpret_cast<const __half2*>(&u), s));
+  }
 }
 
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
@@ -213,7 +230,7 @@ struct Ring {
   }
 };
 
-__global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_constant__ LinearParams P) {
+__global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_constant__ LinearParams P) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ alignas(8) uint64_t bars[B_COUNT];
   __shared__ uint32_t tmem_ptr;
@@ -241,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
   };
   if (threadIdx.x == kConv) {                // the load warp's first lane
     for (int i = 0; i < B_COUNT; ++i)
-      mbar_init(bar(i), i >= B_RE && i < B_AE ? kConv / 32 : 1);
+      mbar_init(bar(i), i < B_RE ? 1 : i < B_AF ? kConv / 32 : i < B_AE ? 4 : 1);
     failed = 0;
     fence_mbar_init();
     for (int i = 0; i < kRaw && i < ne; ++i) load_entry(i, i);   // weights do not wait for the first kernel
@@ -259,44 +276,51 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
 
   if (warp < kConv / 32) {
     // ------------------------------------------------------------------ converting warps
-    // Warp w decodes rows 32 (w % 4) + lane, channels 32 (w / 4) .. + 31 of each
-    // 128: 16 bytes of codes and two scales become 16 packed pairs, which are
-    // 16 columns of the row's TMEM lane.
-    const int r = 32 * (warp & 3) + lane, seg = warp >> 2;
-    const uint32_t a_tmem = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColA + 16u * (uint32_t)seg;
+    // Warps 0-3 take an entry's even chunks, warps 4-7 its odd ones. A thread
+    // decodes one row's chunk: 64 bytes of codes and eight scales become 64 packed
+    // pairs, the 64 columns of an A stage in the row's TMEM lane.
+    const int r = 32 * (warp & 3) + lane, grp = warp >> 2;
+    const uint32_t a_tmem = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColA;
+    const Shifts pw;
     Ring<kRaw> rr;
+    Ring<kA> ra;                             // of chunk 4e + c, c = grp, grp + 2
+    if (grp) ra.step();
     for (int e = 0; e < ne && ok; ++e) {
       ok = __all_sync(0xffffffffu, mbar_wait(bar(B_RF + rr.stage), rr.par));
       if (!ok) break;
       const uint8_t* src = smem + off_raw + rr.stage * kRawBytes + r * kFp4EntryBytes;
+#pragma unroll 1
+      for (int c = grp; c < kPer; c += 2) {
+        uint4 q[4];
 #pragma unroll
-      for (int c = 0; c < kPer; ++c) {
-        const uint4 q = *reinterpret_cast<const uint4*>(src + 64 * c + 16 * seg);
-        const uint32_t sc = *reinterpret_cast<const unsigned short*>(src + kCkv / 2 + 8 * c + 2 * seg);
-        const __half2 s2 = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)sc, __NV_E4M3)),
-                                   __float2half2_rn(128.f));
-        const uint32_t wd[4] = {q.x, q.y, q.z, q.w};
-        uint32_t v[16];
+        for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const uint4*>(src + 64 * c + 16 * i);
+        const uint2 sc = *reinterpret_cast<const uint2*>(src + kCkv / 2 + 8 * c);
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(B_AE + ra.stage), ra.par ^ 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t col = a_tmem + (uint32_t)(ra.stage * kChunkK / 2);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const __half2 s = i < 2 ? __low2half2(s2) : __high2half2(s2);
-          v[4 * i] = decode2<0>(wd[i], s);
-          v[4 * i + 1] = decode2<1>(wd[i], s);
-          v[4 * i + 2] = decode2<2>(wd[i], s);
-          v[4 * i + 3] = decode2<3>(wd[i], s);
+          const uint32_t two = (i < 2 ? sc.x : sc.y) >> (16 * (i & 1));
+          const __half2 s2 = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)),
+                                     __float2half2_rn(128.f));
+          uint32_t v[16];
+          decode8(q[i].x, __low2half2(s2), pw, v);
+          decode8(q[i].y, __low2half2(s2), pw, v + 4);
+          decode8(q[i].z, __high2half2(s2), pw, v + 8);
+          decode8(q[i].w, __high2half2(s2), pw, v + 12);
+          tmem_st16(col + 16u * i, v);
         }
-        if (c == kPer - 1) {                 // the entry is in registers
+        if (c + 2 >= kPer) {                 // the entry is read
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B_RE + rr.stage));
         }
-        if (e > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_AE + c), (uint32_t)(e - 1) & 1u));
-        if (!ok) break;
-        tc_fence_after();
-        tmem_st16(a_tmem + (uint32_t)(c * kChunkK / 2), v);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_AF + c));
+        if (lane == 0) mbar_arrive(bar(B_AF + ra.stage));
+        ra.step();
+        ra.step();
       }
       rr.step();
     }
@@ -331,25 +355,24 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
     const uint32_t el = elect_one();
     const uint32_t idesc = idesc_f16_f32(kRowsM, P.tok_pad);
     Ring<kX> rx;
-    for (int e = 0; e < ne && ok; ++e) {
+    Ring<kA> ra;
+    for (int c = 0; c < ne * kPer; ++c) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(B_XF + rx.stage), rx.par) && mbar_wait(bar(B_AF + ra.stage), ra.par));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t xb = sb0 + off_x + rx.stage * x_bytes;
 #pragma unroll
-      for (int c = 0; c < kPer; ++c) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(B_XF + rx.stage), rx.par) && mbar_wait(bar(B_AF + c), (uint32_t)e & 1u));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t xb = sb0 + off_x + rx.stage * x_bytes;
+      for (int b = 0; b < 2; ++b) {
+        const uint64_t bd = smem_desc(xb + b * P.tok_pad * 128, 16, 1024, kSwizzle128B);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const uint64_t bd = smem_desc(xb + b * P.tok_pad * 128, 16, 1024, kSwizzle128B);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_one(el, tmem, tmem + kColA + (uint32_t)(c * kChunkK / 2 + b * 32 + k * 8), desc_advance(bd, 32 * k),
-                    idesc, e > 0 || c > 0 || b > 0 || k > 0);
-        }
-        commit_one(el, bar(B_AE + c));
-        commit_one(el, bar(B_XE + rx.stage));
-        rx.step();
+        for (int k = 0; k < 4; ++k)
+          mma_one(el, tmem, tmem + kColA + (uint32_t)(ra.stage * kChunkK / 2 + b * 32 + k * 8), desc_advance(bd, 32 * k),
+                  idesc, c > 0 || b > 0 || k > 0);
       }
+      commit_one(el, bar(B_AE + ra.stage));
+      commit_one(el, bar(B_XE + rx.stage));
+      ra.step();
+      rx.step();
     }
     if (ok && ne > 0) commit_one(el, bar(B_DONE));
   }
@@ -363,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
   float* part = reinterpret_cast<float*>(smem);
   if (ne > 0 && !failed && !mbar_wait(bar(B_DONE), 0)) *reinterpret_cast<volatile int*>(&failed) = 1;
   tc_fence_after();
-  for (int c = 16 * (warp >> 2); c < P.tok_pad && warp < kConv / 32; c += 64) {
+  for (int c = 16 * (warp >> 2); c < P.tok_pad && warp < kConv / 32; c += 16 * (kConv / 128)) {
     uint32_t v[16];
     if (ne > 0) {
       tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)c, v);
@@ -478,9 +501,9 @@ cudaError_t launch_fp4_linear(const mla_fp4_linear_args* a, void* ws, int sms, c
   cudaError_t e = cudaLaunchKernelEx(&cfg, x_to_f16, *a, xs, exps);
   if (e != cudaSuccess) return e;
 
-  // K over as many CTAs as there are SMs (a CTA's rings fill one), in entries
+  // K over as many CTAs as two per SM hold, in entries
   const int64_t clusters = (int64_t)a->G * P.tiles * ((T + kTokMax - 1) / kTokMax);
-  int64_t S = sms / clusters;
+  int64_t S = 2 * sms / clusters;
   if (S > a->K / kCkv) S = a->K / kCkv;
   if (S > 8) S = 8;
   if (S < 1) S = 1;
