@@ -16,19 +16,21 @@
 // accumulation. The epilogue takes the power of two out again.
 //
 //   x_to_f16      one CTA per (token, group): largest magnitude, then the row.
-//   fp4_linear    one cluster of S CTAs per 128 output rows and 64 tokens, each a
-//                 range of K in entries of 512 channels, two CTAs per SM. TMA
-//                 brings the rows' 288-byte entries into a ring; 8 warps decode
-//                 them, 128 channels at a time, straight into the A operand in
-//                 tensor memory (through a shared-memory A tile its writes and
-//                 reads were the bound); TMA brings the tokens' B tile; one warp
-//                 issues the MMAs (M = 128, N = tokens). The S partial sums meet
-//                 through distributed shared memory in rank order.
+//   fp4_linear    one cluster of S CTAs per 256 output rows and 64 tokens, each a
+//                 range of K in entries of 512 channels. TMA brings the rows'
+//                 288-byte entries into a ring; 16 warps decode them, 128 channels
+//                 at a time, straight into the A operand in tensor memory (through
+//                 a shared-memory A tile its writes and reads were the bound); TMA
+//                 brings the tokens' B tile, which both halves of the rows share;
+//                 one warp issues the MMAs (M = 128, N = tokens). The S partial
+//                 sums meet through distributed shared memory in rank order.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
 #include <math.h>
 #include <string.h>
+
+#include <mutex>
 
 #include "common.cuh"
 #include "fp4_linear.h"
@@ -39,21 +41,21 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kRowsM = 128;                  // output rows per cluster
+constexpr int kRowsM = 256;                  // output rows per cluster: two halves of an MMA's 128
 constexpr int kTokMax = 64;                  // tokens per cluster
-constexpr int kChunkK = 128;                 // channels per A stage (64 columns) and token tile (two swizzled blocks)
+constexpr int kChunkK = 128;                 // channels per A stage (64 columns a half) and token tile (two swizzled blocks)
 constexpr int kPer = kCkv / kChunkK;         // chunks per entry
 constexpr int kRawBytes = kRowsM * kFp4EntryBytes;
-constexpr int kRaw = 2, kA = 3, kX = 2;      // stages: entries, A chunks, token tiles; two CTAs per SM
-constexpr uint32_t kColA = 64;               // TMEM columns: sums at 0, A stages from 64
-constexpr uint32_t kTmemCols = 256;
-constexpr int kConv = 256;                   // converting threads: two chunks of 128 rows at a time
+constexpr int kRaw = 2, kA = 3, kX = 4;      // stages: entries, A chunks, token tiles
+constexpr uint32_t kColA = 128;              // TMEM columns: the halves' sums at 0 and 64, A stages of 128 from 128
+constexpr uint32_t kTmemCols = 512;
+constexpr int kConv = 512;                   // converting threads: two chunks of 256 rows at a time
 constexpr int kThreads = kConv + 64;         // + load warp + MMA warp
 
 enum : int {
   B_RF = 0,                // [kRaw] entries landed
   B_RE = B_RF + kRaw,      // [kRaw] entries converted (one arrival per converting warp)
-  B_AF = B_RE + kRaw,      // [kA] A stage written (one arrival per warp of four)
+  B_AF = B_RE + kRaw,      // [kA] A stage written (one arrival per warp of eight)
   B_AE = B_AF + kA,        // [kA] MMAs over the A stage done
   B_XF = B_AE + kA,        // [kX] token tile landed
   B_XE = B_XF + kX,        // [kX] MMAs over the token tile done
@@ -63,7 +65,7 @@ enum : int {
 
 struct alignas(64) LinearParams {
   CUtensorMap tm_x;                          // scaled activations (K, T, G) float16, box 64 x tokens
-  CUtensorMap tm_w;                          // entries as (words of a row, N, G), box 72 words x 128 rows
+  CUtensorMap tm_w;                          // entries as (words of a row, N, G), box 72 words x 256 rows
   const int* exps;                           // (G, T): token t's row holds x 2^-exps
   __nv_bfloat16* out;
   int T, G, N, K;
@@ -230,7 +232,7 @@ struct Ring {
   }
 };
 
-__global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_constant__ LinearParams P) {
+__global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_constant__ LinearParams P) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ alignas(8) uint64_t bars[B_COUNT];
   __shared__ uint32_t tmem_ptr;
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_co
   uint32_t S;
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(S));
   const uint32_t rank = cluster_ctarank();
-  const int tile = blockIdx.x / S;           // (group, 128 rows)
+  const int tile = blockIdx.x / S;           // (group, 256 rows)
   const int g = tile / P.tiles, n0 = (tile - g * P.tiles) * kRowsM;
   const int t0 = blockIdx.y * kTokMax;
   const int entries = P.K / kCkv;
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_co
   };
   if (threadIdx.x == kConv) {                // the load warp's first lane
     for (int i = 0; i < B_COUNT; ++i)
-      mbar_init(bar(i), i < B_RE ? 1 : i < B_AF ? kConv / 32 : i < B_AE ? 4 : 1);
+      mbar_init(bar(i), i < B_RE ? 1 : i < B_AF ? kConv / 32 : i < B_AE ? kConv / 64 : 1);
     failed = 0;
     fence_mbar_init();
     for (int i = 0; i < kRaw && i < ne; ++i) load_entry(i, i);   // weights do not wait for the first kernel
@@ -276,11 +278,12 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_co
 
   if (warp < kConv / 32) {
     // ------------------------------------------------------------------ converting warps
-    // Warps 0-3 take an entry's even chunks, warps 4-7 its odd ones. A thread
+    // Warps 0-7 decode rows 0-127, 8-15 the others; of either eight the first four
+    // take an entry's even chunks, the last four its odd ones. A thread
     // decodes one row's chunk: 64 bytes of codes and eight scales become 64 packed
     // pairs, the 64 columns of an A stage in the row's TMEM lane.
-    const int r = 32 * (warp & 3) + lane, grp = warp >> 2;
-    const uint32_t a_tmem = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColA;
+    const int half = warp >> 3, r = 128 * half + 32 * (warp & 3) + lane, grp = (warp >> 2) & 1;
+    const uint32_t a_tmem = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColA + 64u * (uint32_t)half;
     const Shifts pw;
     Ring<kRaw> rr;
     Ring<kA> ra;                             // of chunk 4e + c, c = grp, grp + 2
@@ -298,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_co
         ok = __all_sync(0xffffffffu, mbar_wait(bar(B_AE + ra.stage), ra.par ^ 1));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t col = a_tmem + (uint32_t)(ra.stage * kChunkK / 2);
+        const uint32_t col = a_tmem + (uint32_t)(ra.stage * kChunkK);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t two = (i < 2 ? sc.x : sc.y) >> (16 * (i & 1));
@@ -353,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_co
   } else {
     // ------------------------------------------------------------------ MMA issue
     const uint32_t el = elect_one();
-    const uint32_t idesc = idesc_f16_f32(kRowsM, P.tok_pad);
+    const uint32_t idesc = idesc_f16_f32(128, P.tok_pad);
     Ring<kX> rx;
     Ring<kA> ra;
     for (int c = 0; c < ne * kPer; ++c) {
@@ -366,8 +369,10 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_co
         const uint64_t bd = smem_desc(xb + b * P.tok_pad * 128, 16, 1024, kSwizzle128B);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_one(el, tmem, tmem + kColA + (uint32_t)(ra.stage * kChunkK / 2 + b * 32 + k * 8), desc_advance(bd, 32 * k),
-                  idesc, c > 0 || b > 0 || k > 0);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            mma_one(el, tmem + 64u * h, tmem + kColA + (uint32_t)(ra.stage * kChunkK + 64 * h + b * 32 + k * 8),
+                    desc_advance(bd, 32 * k), idesc, c > 0 || b > 0 || k > 0);
       }
       commit_one(el, bar(B_AE + ra.stage));
       commit_one(el, bar(B_XE + rx.stage));
@@ -386,25 +391,26 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_co
   float* part = reinterpret_cast<float*>(smem);
   if (ne > 0 && !failed && !mbar_wait(bar(B_DONE), 0)) *reinterpret_cast<volatile int*>(&failed) = 1;
   tc_fence_after();
-  for (int c = 16 * (warp >> 2); c < P.tok_pad && warp < kConv / 32; c += 16 * (kConv / 128)) {
+  const int half = warp >> 3;
+  for (int c = 16 * ((warp >> 2) & 1); c < P.tok_pad && warp < kConv / 32; c += 32) {
     uint32_t v[16];
     if (ne > 0) {
-      tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)c, v);
+      tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(64 * half + c), v);
       tmem_wait_ld();
     } else {
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = 0u;
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) part[(c + i) * kRowsM + 32 * (warp & 3) + lane] = __uint_as_float(v[i]);
+    for (int i = 0; i < 16; ++i) part[(c + i) * kRowsM + 128 * half + 32 * (warp & 3) + lane] = __uint_as_float(v[i]);
   }
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && failed && P.err) atomicOr(P.err, MLA_DEVICE_ERR_TIMEOUT);
   cluster_sync();
   const int nt = min(P.tok_pad, P.T - t0);
-  for (int i = warp * (int)S + (int)rank; i < nt && warp < kConv / 32; i += kConv / 32 * (int)S) {
-    const uint32_t mine = smem_u32(part + i * kRowsM + 4 * lane);
+  for (int i = (warp & 7) * (int)S + (int)rank; i < nt && warp < kConv / 32; i += kConv / 64 * (int)S) {
+    const uint32_t mine = smem_u32(part + i * kRowsM + 128 * half + 4 * lane);
     float4 v[8];
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k)
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_linear_kernel(const __grid_co
       if (k < S) sum = make_float4(sum.x + v[k].x, sum.y + v[k].y, sum.z + v[k].z, sum.w + v[k].w);
     const double f = ldexp((double)P.scale, P.exps[g * P.T + t0 + i] + 7);
     const float y[4] = {(float)(sum.x * f), (float)(sum.y * f), (float)(sum.z * f), (float)(sum.w * f)};
-    const int n = n0 + 4 * lane;
+    const int n = n0 + 128 * half + 4 * lane;
     __nv_bfloat16* out = P.out + (int64_t)(t0 + i) * P.G * P.N + (int64_t)g * P.N + n;
     if (n + 3 < P.N && (reinterpret_cast<uintptr_t>(out) & 7u) == 0) {
       *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
@@ -442,6 +448,58 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
   }();
   return fn;
+}
+
+size_t smem_bytes(int tok_pad) { return (size_t)kRaw * kRawBytes + (size_t)kX * tok_pad * kChunkK * 2 + 1024; }
+
+// CTAs per cluster (ranges of K). Clusters of S stay within a GPC, so how many
+// of them run at once is the device's answer, asked once per device and shared
+// memory size: 74, 33, 22, 15 clusters of 2, 4, 6, 8 on a B200. The count taken
+// minimises waves x (entries per CTA + kFixed), kFixed being what a CTA spends
+// besides its entries (launch, first load, exchange), in entries.
+cudaError_t pick_splits(int64_t clusters, int entries, int tok_pad, int* out) {
+  constexpr int kMaxS = 8, kMaxDev = 64, kFixed = 4;
+  static std::mutex mu;
+  static int active[kMaxDev][kTokMax / 16][kMaxS];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  int* act = active[dev][tok_pad / 16 - 1];
+  if (!act[0]) {
+    const size_t smem = smem_bytes(tok_pad);
+    // the largest size any call needs: the attribute is set once for all of them
+    e = cudaFuncSetAttribute(fp4_linear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(kTokMax));
+    if (e != cudaSuccess) return e;
+    for (int S = kMaxS; S >= 1; --S) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = (unsigned)S;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3((unsigned)(S * 64));
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = smem;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, fp4_linear_kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      act[S - 1] = n;                        // [0] last: a filled table
+    }
+    if (act[0] < 1) return cudaErrorInvalidConfiguration;
+  }
+  int64_t best = 0;
+  for (int S = 1; S <= kMaxS && S <= entries; ++S) {
+    if (act[S - 1] < 1) continue;
+    const int64_t cost = (clusters + act[S - 1] - 1) / act[S - 1] * ((entries + S - 1) / S + kFixed);
+    if (S == 1 || cost < best) {
+      best = cost;
+      *out = S;
+    }
+  }
+  return cudaSuccess;
 }
 
 size_t xs_bytes(const mla_fp4_linear_args* a) {
@@ -501,14 +559,10 @@ cudaError_t launch_fp4_linear(const mla_fp4_linear_args* a, void* ws, int sms, c
   cudaError_t e = cudaLaunchKernelEx(&cfg, x_to_f16, *a, xs, exps);
   if (e != cudaSuccess) return e;
 
-  // K over as many CTAs as two per SM hold, in entries
   const int64_t clusters = (int64_t)a->G * P.tiles * ((T + kTokMax - 1) / kTokMax);
-  int64_t S = 2 * sms / clusters;
-  if (S > a->K / kCkv) S = a->K / kCkv;
-  if (S > 8) S = 8;
-  if (S < 1) S = 1;
-  const size_t smem = (size_t)kRaw * kRawBytes + (size_t)kX * P.tok_pad * kChunkK * 2 + 1024;
-  e = cudaFuncSetAttribute(fp4_linear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const size_t smem = smem_bytes(P.tok_pad);
+  int S = 0;
+  e = pick_splits(clusters, a->K / kCkv, P.tok_pad, &S);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)((int64_t)a->G * P.tiles * S), (unsigned)((T + kTokMax - 1) / kTokMax));
   cfg.blockDim = dim3(kThreads);
