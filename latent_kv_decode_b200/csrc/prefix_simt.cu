@@ -2,53 +2,112 @@
 // inputs (which need full precision) and of page sizes that the tensor-core
 // kernel does not take.
 //
-// A CTA owns 32 stacked rows and a range of their 32-token tiles. Per tile:
-//   S = Q . K^T    four groups of 64 threads take a quarter of the 576-wide dot
-//                  each, 4 x 4 scores per thread; the quarters are summed by
-//                  the softmax.
-//   softmax        warp w keeps the online statistics of rows 4w .. 4w+3, lane
-//                  = token.
-//   O += P . V     thread = 8 rows x 8 columns of the 32 x 512 accumulator.
-// Both products read 16-byte vectors of shared memory, 8 (S) and 16 (O) FMA per
-// vector.
+// A CTA owns 32 stacked rows and a range of their 16-token tiles, two of which
+// are in flight: the next tile's rows arrive (cp.async) while this one computes.
+//   S = Q . K^T    eight groups of 64 threads take an eighth of the 576-wide dot
+//                  each, 4 x 2 scores per thread; the parts are summed by the
+//                  softmax.
+//   softmax        warp w keeps the online statistics of rows 2w and 2w+1, a lane
+//                  per token.
+//   O += P . V     thread = 8 rows x 4 columns of the 32 x 512 accumulator.
+// Both products are packed float32 FMAs (two per instruction: the plain ones
+// reach half the rate on sm_100) on 16-byte vectors of shared memory.
 //
 // Tokens that no row may see are zeros in the tile, so whatever their cache
 // rows hold stays out of the sums; where a tile that some rows do not see holds
-// an infinity or NaN, the rows whose weight is 0 skip it.
+// an infinity or NaN (its scores show it), the rows whose weight is 0 skip it.
 #include "prefix.h"
+#include "sm100_ptx.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int kRows = 32, kToks = 32;
+constexpr int kRows = 32, kToks = 16;
+constexpr int kThr = 512, kWarps = kThr / 32, kParts = kThr / 64;   // kParts slices of the dot product
 constexpr int kPad = 4;             // floats of row padding: 16-byte rows, 8 rows over all banks
 constexpr int kPart = kToks + 1;
 
 __host__ __device__ constexpr int pitch_of(int D) { return D + kPad; }
 
-template <typename T> __device__ __forceinline__ float4 load4(const T* p);
-template <> __device__ __forceinline__ float4 load4<float>(const float* p) {
-  return *reinterpret_cast<const float4*>(p);
+using f32x2 = unsigned long long;                // two floats, the first in the low half
+struct alignas(16) f32x4 { f32x2 lo, hi; };
+
+__device__ __forceinline__ void fma2(f32x2& acc, f32x2 a, f32x2 b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
 }
-template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+
+// 16 bytes from global to shared memory, or zeros
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory"); }
+
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
   const uint2 u = *reinterpret_cast<const uint2*>(p);
   return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
                      __uint_as_float(u.y & 0xffff0000u));
 }
 
+// Rows of D = Ckv + Dr elements into shared memory as float32; row r comes from
+// lat(r) and pe(r), zeros where lat(r) is null. Asynchronous for float32.
+template <typename T, int kN, typename Lat, typename Pe>
+__device__ __forceinline__ void load_rows(float* dst, int D, Lat lat, Pe pe) {
+  const int d4 = D / 4, pitch = pitch_of(D), lane = threadIdx.x & 31;
+  for (int r = threadIdx.x >> 5; r < kN; r += kWarps) {
+    const T* l = lat(r);
+    const T* e = l ? pe(r) - kCkv : nullptr;
+    float* d = dst + r * pitch;
+    if constexpr (sizeof(T) == 4) {
+      const T* any = lat(-1);
+#pragma unroll
+      for (int u = 0; u < 5; ++u) {
+        const int k = 4 * (lane + 32 * u);
+        if (k < D) copy16(d + k, !l ? any : k < kCkv ? l + k : e + k, l != nullptr);
+      }
+    } else {
+      float4 v[5];
+#pragma unroll
+      for (int u = 0; u < 5; ++u) {
+        const int k = 4 * (lane + 32 * u);
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (l && k < D) v[u] = load4(k < kCkv ? l + k : e + k);
+      }
+#pragma unroll
+      for (int u = 0; u < 5; ++u)
+        if (lane + 32 * u < d4) *reinterpret_cast<float4*>(d + 4 * (lane + 32 * u)) = v[u];
+    }
+  }
+}
+
 template <typename T>
-__global__ void __launch_bounds__(256) prefix_simt(const PrefixParams p) {
+__global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
   extern __shared__ float smem[];
+  __shared__ const T* row_lat[2][kToks];         // the tile's cache rows, null where no row may see the token
+  __shared__ const T* row_pe[2][kToks];
   const int D = p.D, pitch = pitch_of(D);
   float* qs = smem;                              // [kRows][pitch]
-  float* ks = qs + kRows * pitch;                // [kToks][pitch]
-  float* part = ks + kToks * pitch;              // [4][kRows][kPart] quarter scores
-  float* ps = part + 4 * kRows * kPart;          // [kToks][kRows] probabilities
-  float* alpha = ps + kToks * kRows;             // [kRows]
+  float* ks = qs + kRows * pitch;                // [2][kToks][pitch]
+  float* part = ks + 2 * kToks * pitch;          // [kParts][kRows][kPart] parts of the scores
+  f32x2* ps = reinterpret_cast<f32x2*>(part + kParts * kRows * kPart);   // [kToks][kRows] weights, twice each
+  float* alpha = reinterpret_cast<float*>(ps + kToks * kRows);           // [kRows]
   float* stat = alpha + kRows;                   // [kRows] 1 / denominator
-  int* tok_ok = reinterpret_cast<int*>(stat + kRows);   // [kToks] some row may see the token
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  sm100::pdl_launch_dependents();
+  sm100::pdl_wait();
   const int r0 = blockIdx.x * kRows, z = blockIdx.y;
   const int nr = min(kRows, p.N - r0);
   const int b0 = r0 / p.HQ, b1 = (r0 + nr - 1) / p.HQ;
@@ -56,171 +115,174 @@ __global__ void __launch_bounds__(256) prefix_simt(const PrefixParams p) {
   const int per = (tiles + p.num_splits - 1) / p.num_splits;
   const int j0 = min(tiles, z * per), j1 = min(tiles, j0 + per);
 
-  const int d4 = D / 4;
-  for (int i = tid; i < kRows * d4; i += 256) {
-    const int r = i / d4, k = 4 * (i - r * d4);
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < nr)
-      v = k < p.Ckv ? load4(reinterpret_cast<const T*>(p.q_lat) + (int64_t)(r0 + r) * p.Ckv + k)
-                    : load4(reinterpret_cast<const T*>(p.q_pe) + (int64_t)(r0 + r) * p.Dr + (k - p.Ckv));
-    *reinterpret_cast<float4*>(qs + r * pitch + k) = v;
-  }
+  const T* q_lat = reinterpret_cast<const T*>(p.q_lat) + (int64_t)r0 * p.Ckv;
+  const T* q_pe = reinterpret_cast<const T*>(p.q_pe) + (int64_t)r0 * p.Dr;
+  load_rows<T, kRows>(qs, D, [&](int r) { return r < nr ? q_lat + (int64_t)max(r, 0) * p.Ckv : nullptr; },
+                      [&](int r) { return q_pe + (int64_t)r * p.Dr; });
 
-  // S: thread (ty, tx) of quarter kq holds rows ty + 8i, tokens tx + 8j
-  const int kq = tid >> 6, ty = (tid >> 3) & 7, tx = tid & 7;
-  const int kq4 = d4 / 4;                        // float4 steps per quarter (D is a multiple of 16)
-  // softmax: rows 4 warp + i, lane = token
-  float m_run[4], l_run[4];
-  int row_b[4], row_lim[4];                      // sequence and last visible own token of the row
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    m_run[i] = -INFINITY;
-    l_run[i] = 0.f;
-    const int r = r0 + 4 * warp + i;
-    row_b[i] = r < p.N ? r / p.HQ : -2;
-    row_lim[i] = 0x7fffffff;
-    if (r < p.N && p.causal) row_lim[i] = prefix_len_of(p, row_b[i]) - p.Q + r % p.Q;
-  }
-  // O: rows 8 rg + i, columns 4 cg + k and 256 + 4 cg + k
-  const int rg = tid >> 6, cg = tid & 63;
-  float acc[8][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc[i][k] = 0.f;
-
-  TileWalk<kToks> w;
-  w.seek(p, b0, b1, j0);
-  for (int j = j0; j < j1; ++j) {
-    // a token's cache row; the base pointers are those of the tile's source
+  // the rows of tile `w` into buffer s (after a barrier that follows its last use)
+  auto locate = [&](const TileWalk<kToks>& w, int s) {
+    if (tid >= kToks) return;
     const bool pre = w.b < 0;
-    const T* kvp = reinterpret_cast<const T*>(pre ? p.pkv : p.kv);
-    const T* pep = reinterpret_cast<const T*>(pre ? p.ppe : p.pe);
-    const int64_t kvs = pre ? p.pkv_row : p.kv_row, pes = pre ? p.ppe_row : p.pe_row;
+    const int t = w.t + tid;
     const int32_t* table = pre ? p.ptable : p.table ? p.table + (int64_t)w.b * p.max_pages : nullptr;
-    const int pages = pre ? p.p_pages : p.num_pages;
+    bool ok = t < w.end && (!p.mask || p.mask[(pre ? 0 : p.Lp) + t] != 0);
+    int64_t row = t;
+    if (ok && table) {
+      const int page = table[t / p.page_size];
+      ok = page >= 0 && page < (pre ? p.p_pages : p.num_pages);
+      row = (int64_t)page * p.page_size + t % p.page_size;
+      if (!ok) prefix_flag(p, MLA_DEVICE_ERR_BLOCK_TABLE);
+    }
+    const T* kv = reinterpret_cast<const T*>(pre ? p.pkv : p.kv);
+    const T* pe = reinterpret_cast<const T*>(pre ? p.ppe : p.pe);
     if (!pre && !table) {
-      kvp += w.b * p.kv_batch;
-      pep += w.b * p.pe_batch;
+      kv += w.b * p.kv_batch;
+      pe += w.b * p.pe_batch;
     }
-    const int pos0 = (pre ? 0 : p.Lp) + w.t;     // position of the tile's first token
-    __syncthreads();                             // the last tile's readers are done
-    bool odd = false;                            // this thread loaded an infinity or NaN
-    for (int i = tid; i < kToks * d4; i += 256) {
-      const int tt = i / d4, k = 4 * (i - tt * d4);
-      const int t = w.t + tt;
-      bool ok = t < w.end && (!p.mask || p.mask[pos0 + tt] != 0);
-      int64_t row = t;
-      if (ok && table) {
-        const int page = table[t / p.page_size];
-        ok = page >= 0 && page < pages;
-        row = (int64_t)page * p.page_size + t % p.page_size;
-        if (!ok) prefix_flag(p, MLA_DEVICE_ERR_BLOCK_TABLE);
-      }
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (ok) v = k < p.Ckv ? load4(kvp + row * kvs + k) : load4(pep + row * pes + (k - p.Ckv));
-      odd = odd || !isfinite(v.x) || !isfinite(v.y) || !isfinite(v.z) || !isfinite(v.w);
-      *reinterpret_cast<float4*>(ks + tt * pitch + k) = v;
-      if (k == 0) tok_ok[tt] = ok;
-    }
-    const bool any_odd = __syncthreads_or(odd);
-    {
-      float s[4][4] = {};
-      const float* qp = qs + ty * pitch + 4 * kq * kq4;
-      const float* kp = ks + tx * pitch + 4 * kq * kq4;
-#pragma unroll 2
-      for (int k = 0; k < kq4; ++k) {
-        float4 qv[4], kv[4];
+    row_lat[s][tid] = ok ? kv + row * (pre ? p.pkv_row : p.kv_row) : nullptr;
+    row_pe[s][tid] = pe + row * (pre ? p.ppe_row : p.pe_row);
+  };
+  auto fetch = [&](int s) {
+    load_rows<T, kToks>(ks + s * kToks * pitch, D, [&](int r) { return r < 0 ? q_lat : row_lat[s][r]; },
+                        [&](int r) { return row_pe[s][r]; });
+  };
+  TileWalk<kToks> w, wn;                         // this tile and the next
+  w.seek(p, b0, b1, j0);
+  wn = w;
+  if (j0 < j1) {
+    locate(w, 0);
+    __syncthreads();
+    fetch(0);
+    wn.next(p, b0);
+  }
+  copy_commit();
+
+  // S: thread (ty, tx) of part kq holds rows ty + 8i, tokens tx + 8n
+  const int kq = tid >> 6, ty = (tid >> 3) & 7, tx = tid & 7;
+  const int kq4 = D / (4 * kParts);              // float4 steps per part (D is a multiple of 32)
+  // softmax: row 2 warp + lane / 16, token lane % 16
+  const int sub = lane >> 4, tok = lane & 15;
+  const int srow = 2 * warp + sub;
+  float m_run = -INFINITY, l_run = 0.f;
+  const int row_b = r0 + srow < p.N ? (r0 + srow) / p.HQ : -2;
+  int row_lim = 0x7fffffff;                      // last visible own token of the row
+  if (row_b >= 0 && p.causal) row_lim = prefix_len_of(p, row_b) - p.Q + (r0 + srow) % p.Q;
+  // O: rows 8 rg + i, columns 4 cg + k
+  const int rg = tid >> 7, cg = tid & 127;
+  f32x2 acc[8][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          qv[i] = *reinterpret_cast<const float4*>(qp + 8 * i * pitch + 4 * k);
-          kv[i] = *reinterpret_cast<const float4*>(kp + 8 * i * pitch + 4 * k);
-        }
+  for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = 0ull;
+
+  for (int j = j0; j < j1; ++j) {
+    const int buf = (j - j0) & 1;
+    const bool more = j + 1 < j1;
+    if (more) locate(wn, buf ^ 1);
+    copy_wait<0>();
+    __syncthreads();                             // this tile is in, the next one's rows are known, the other buffer is free
+    if (more) fetch(buf ^ 1);
+    copy_commit();
+    const float* kt = ks + buf * kToks * pitch;
+    const bool pre = w.b < 0;
+    bool odd = false;                            // a non-finite score: a non-finite key
+    {
+      f32x2 s[4][2] = {};                          // sums over even and odd channels
+      const float* qp = qs + ty * pitch + 4 * kq * kq4;
+      const float* kp = kt + tx * pitch + 4 * kq * kq4;
+#pragma unroll 3
+      for (int k = 0; k < kq4; ++k) {
+        f32x4 qv[4], kv[2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const f32x4*>(qp + 8 * i * pitch + 4 * k);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) kv[n] = *reinterpret_cast<const f32x4*>(kp + 8 * n * pitch + 4 * k);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            s[i][n] = fmaf(qv[i].x, kv[n].x, s[i][n]);
-            s[i][n] = fmaf(qv[i].y, kv[n].y, s[i][n]);
-            s[i][n] = fmaf(qv[i].z, kv[n].z, s[i][n]);
-            s[i][n] = fmaf(qv[i].w, kv[n].w, s[i][n]);
+          for (int n = 0; n < 2; ++n) {
+            fma2(s[i][n], qv[i].lo, kv[n].lo);
+            fma2(s[i][n], qv[i].hi, kv[n].hi);
           }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int n = 0; n < 4; ++n) part[(kq * kRows + ty + 8 * i) * kPart + tx + 8 * n] = s[i][n];
+        for (int n = 0; n < 2; ++n) {
+          const float2 v = unpack2(s[i][n]);
+          part[(kq * kRows + ty + 8 * i) * kPart + tx + 8 * n] = v.x + v.y;
+          odd = odd || !isfinite(v.x + v.y);
+        }
     }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 4 * warp + i;
-      const int t = w.t + lane;
+    const bool any_odd = __syncthreads_or(odd);
+    {
+      const int t = w.t + tok;
       // own tokens are seen by their sequence's rows; a causal row sees own
       // tokens up to row_lim (a negative one reaches back into the prefix)
-      bool vis = tok_ok[lane] != 0 && row_b[i] >= 0 && (pre || row_b[i] == w.b);
-      vis = vis && (!p.causal || (pre ? t - p.Lp : t) <= row_lim[i]);
-      float s = -INFINITY;
-      if (vis)
-        s = ((part[r * kPart + lane] + part[(kRows + r) * kPart + lane]) +
-             (part[(2 * kRows + r) * kPart + lane] + part[(3 * kRows + r) * kPart + lane])) * p.scale;
+      bool vis = row_lat[buf][tok] != nullptr && row_b >= 0 && (pre || row_b == w.b);
+      vis = vis && (!p.causal || (pre ? t - p.Lp : t) <= row_lim);
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) s += part[(k * kRows + srow) * kPart + tok];
+      s = vis ? s * p.scale : -INFINITY;
       float mx = s;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float m_new = fmaxf(m_run[i], mx);
-      const float al = m_run[i] == -INFINITY ? 0.f : expf(m_run[i] - m_new);
+      for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float m_new = fmaxf(m_run, mx);
+      const float al = m_run == -INFINITY ? 0.f : expf(m_run - m_new);
       const float e = vis ? expf(s - m_new) : 0.f;
       float sum = e;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      l_run[i] = l_run[i] * al + sum;
-      m_run[i] = m_new;
-      ps[lane * kRows + r] = e;
-      if (lane == 0) alpha[r] = al;
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      l_run = l_run * al + sum;
+      m_run = m_new;
+      ps[tok * kRows + srow] = pack2(e, e);
+      if (tok == 0) alpha[srow] = al;
     }
     __syncthreads();
-    float al[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) al[i] = alpha[8 * rg + i];
+    for (int i = 0; i < 8; ++i) {
+      const float al = alpha[8 * rg + i];
+      const f32x2 al2 = pack2(al, al);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+      for (int k = 0; k < 2; ++k) asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(acc[i][k]) : "l"(al2));
+    }
+    if (!any_odd) {
+#pragma unroll 4
+      for (int tt = 0; tt < kToks; ++tt) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 4 * cg);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[i][k] *= al[i];
-#pragma unroll 2
-    for (int tt = 0; tt < kToks; ++tt) {
-      const float4 p0 = *reinterpret_cast<const float4*>(ps + tt * kRows + 8 * rg);
-      const float4 p1 = *reinterpret_cast<const float4*>(ps + tt * kRows + 8 * rg + 4);
-      const float4 v0 = *reinterpret_cast<const float4*>(ks + tt * pitch + 4 * cg);
-      const float4 v1 = *reinterpret_cast<const float4*>(ks + tt * pitch + 256 + 4 * cg);
-      const float pr[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-      const float vv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-      if (!any_odd) {
+        for (int i = 0; i < 8; i += 2) {
+          const f32x4 pr = *reinterpret_cast<const f32x4*>(ps + tt * kRows + 8 * rg + i);
+          fma2(acc[i][0], pr.lo, v.lo);
+          fma2(acc[i][1], pr.lo, v.hi);
+          fma2(acc[i + 1][0], pr.hi, v.lo);
+          fma2(acc[i + 1][1], pr.hi, v.hi);
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int tt = 0; tt < kToks; ++tt) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 4 * cg);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) acc[i][k] = fmaf(pr[i], vv[k], acc[i][k]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) acc[i][k] = pr[i] != 0.f ? fmaf(pr[i], vv[k], acc[i][k]) : acc[i][k];
+        for (int i = 0; i < 8; ++i) {
+          const f32x2 pr = ps[tt * kRows + 8 * rg + i];
+          if (pr != 0ull) {
+            fma2(acc[i][0], pr, v.lo);
+            fma2(acc[i][1], pr, v.hi);
+          }
+        }
       }
     }
-    w.next(p, b0);
+    w = wn;
+    if (more) wn.next(p, b0);
   }
 
   // the rows' denominators to the accumulator's threads
   const bool split = p.num_splits > 1;
   __syncthreads();
-  if (lane < 4) {
-    float m = m_run[0], l = l_run[0];
-#pragma unroll
-    for (int i = 1; i < 4; ++i)
-      if (lane == i) {
-        m = m_run[i];
-        l = l_run[i];
-      }
-    const int r = r0 + 4 * warp + lane;
+  {
+    float m = m_run, l = l_run;
+    const int r = r0 + srow;
     float inv = 0.f;
     if (r < p.N) {
       float wt = 1.f;
@@ -233,12 +295,14 @@ __global__ void __launch_bounds__(256) prefix_simt(const PrefixParams p) {
       const bool seen = !(m == -INFINITY && l == 0.f);   // a NaN denominator stays one
       inv = seen ? wt / l : 0.f;
       const float lse = seen ? m + logf(l) : -INFINITY;
-      if (split)
-        p.ws_lse[(int64_t)z * p.N + r] = lse;
-      else if (p.lse)
-        p.lse[r] = lse;
+      if (tok == 0) {
+        if (split)
+          p.ws_lse[(int64_t)z * p.N + r] = lse;
+        else if (p.lse)
+          p.lse[r] = lse;
+      }
     }
-    stat[4 * warp + lane] = inv;
+    if (tok == 0) stat[r - r0] = inv;
   }
   __syncthreads();
 #pragma unroll
@@ -246,15 +310,16 @@ __global__ void __launch_bounds__(256) prefix_simt(const PrefixParams p) {
     const int r = r0 + 8 * rg + i;
     if (r >= p.N) continue;
     const float inv = stat[8 * rg + i];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int c = (k < 4 ? 0 : 256) + 4 * cg + (k & 3);
-      const float v = inv == 0.f ? 0.f : acc[i][k] * inv;
-      if (split)
-        p.ws_o[((int64_t)z * p.N + r) * p.Ckv + c] = v;
-      else
-        reinterpret_cast<T*>(p.x)[(int64_t)r * p.Ckv + c] = from_f32<T>(v);
-    }
+    const float2 lo = unpack2(acc[i][0]), hi = unpack2(acc[i][1]);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (inv != 0.f) v = make_float4(lo.x * inv, lo.y * inv, hi.x * inv, hi.y * inv);
+    if (split)
+      *reinterpret_cast<float4*>(p.ws_o + ((int64_t)z * p.N + r) * p.Ckv + 4 * cg) = v;
+    else if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float4*>(reinterpret_cast<T*>(p.x) + (int64_t)r * p.Ckv + 4 * cg) = v;
+    else
+      *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.x) + (int64_t)r * p.Ckv + 4 * cg) =
+          make_uint2(sm100::pack_bf16(v.x, v.y), sm100::pack_bf16(v.z, v.w));
   }
 }
 
@@ -263,24 +328,34 @@ cudaError_t launch(const PrefixParams& p, cudaStream_t st) {
   const size_t smem = prefix_simt_smem(p.D);
   cudaError_t e = cudaFuncSetAttribute(prefix_simt<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  prefix_simt<T><<<dim3((p.N + kRows - 1) / kRows, p.num_splits), 256, smem, st>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.N + kRows - 1) / kRows), (unsigned)p.num_splits);
+  cfg.blockDim = dim3(kThr);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, prefix_simt<T>, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
 size_t prefix_simt_smem(int D) {
-  return sizeof(float) * ((size_t)(kRows + kToks) * pitch_of(D) + 4 * kRows * kPart + kToks * kRows + 2 * kRows) +
-         sizeof(int) * kToks;
+  return sizeof(float) * ((size_t)(kRows + 2 * kToks) * pitch_of(D) + kParts * kRows * kPart + 2 * kToks * kRows + 2 * kRows);
 }
 
-// about one CTA per SM (its shared memory fills one), no split shorter than a tile
+// about one CTA per SM (its shared memory fills one), at least four tiles each:
+// a split costs a merge of about 3 us, a tile takes 2.2
 int prefix_simt_auto_splits(const mla_prefix_args* a, int sms) {
   const int64_t rows = (int64_t)a->B * a->H * a->Q;
   const int64_t blocks = (rows + kRows - 1) / kRows;
   const int64_t tiles = ((int64_t)a->prefix_len + kToks - 1) / kToks + (a->Lk + kToks - 1) / kToks;
   int64_t s = sms / blocks;
-  if (s > tiles) s = tiles;
+  if (s > tiles / 4) s = tiles / 4;
   if (s > 64) s = 64;
   return s < 1 ? 1 : (int)s;
 }
