@@ -343,8 +343,8 @@ mla_status_t mla_group_wo(const mla_group_wo_args* a, void* workspace, size_t wo
  *     cu_tokens == NULL: sequence b owns rows [b*Q, (b+1)*Q), N = B*Q.
  *     cu_tokens (B+1) int32, non-decreasing: sequence b owns rows
  *     [cu_tokens[b], cu_tokens[b+1]) (none is allowed); rows outside
- *     [cu_tokens[0], cu_tokens[B]) belong to no sequence: nothing is read
- *     from or written for them. Q is then ignored.
+ *     [cu_tokens[0], cu_tokens[B]) belong to no sequence: nothing is
+ *     written for them. Q is then ignored.
  *   seq_lens (B) int32, required: the lengths AFTER the append. The i-th of a
  *     sequence's n new tokens is token t = seq_lens[b] - n + i and goes to the
  *     row mla_decode reads for t (kv_cache / pe_cache, strides, Lk,

@@ -16,6 +16,7 @@
 // Tokens that no row may see are zeros in the tile, so whatever their cache
 // rows hold stays out of the sums; where a tile that some rows do not see holds
 // an infinity or NaN (its scores show it), the rows whose weight is 0 skip it.
+#include "once_per_device.h"
 #include "prefix.h"
 #include "sm100_ptx.cuh"
 
@@ -326,7 +327,10 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
 template <typename T>
 cudaError_t launch(const PrefixParams& p, cudaStream_t st) {
   const size_t smem = prefix_simt_smem(p.D);
-  cudaError_t e = cudaFuncSetAttribute(prefix_simt<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static OncePerDevice smem_set;
+  cudaError_t e = smem_set([] {
+    return cudaFuncSetAttribute(prefix_simt<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prefix_simt_smem(kCkv + 64));
+  });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((p.N + kRows - 1) / kRows), (unsigned)p.num_splits);

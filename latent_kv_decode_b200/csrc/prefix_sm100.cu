@@ -43,6 +43,7 @@
 #include <math.h>
 #include <string.h>
 
+#include "once_per_device.h"
 #include "prefix.h"
 #include "sm100_ptx.cuh"
 
@@ -785,11 +786,15 @@ bool encode_source(CUtensorMap* kv, CUtensorMap* kx, CUtensorMap* pe, const void
 bool prefix_sm100_supported(const mla_prefix_args* a) {
   if (a->dtype != MLA_BF16) return false;
   if ((a->prefix_table || a->block_table) && a->page_size % 64 != 0) return false;
-  int dev = 0, major = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-    return false;
-  return major == 10 && encode_fn() != nullptr;
+  static OncePerDevice sm100;
+  return encode_fn() != nullptr && sm100([] {
+           int dev = 0, major = 0;
+           const cudaError_t e = cudaGetDevice(&dev);
+           if (e != cudaSuccess) return e;
+           return cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) == cudaSuccess && major == 10
+                      ? cudaSuccess
+                      : cudaErrorNotSupported;
+         }) == cudaSuccess;
 }
 
 int prefix_sm100_auto_splits(const mla_prefix_args* a, int sms) {
@@ -830,7 +835,10 @@ cudaError_t launch_prefix_sm100(const PrefixParams& p, cudaStream_t st) {
                        rows, p.table ? p.num_pages : p.B, p.Dr))
       return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(prefix_sm100_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+  static OncePerDevice smem_set;
+  cudaError_t e = smem_set([] {
+    return cudaFuncSetAttribute(prefix_sm100_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+  });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * P.blocks * p.num_splits));
