@@ -4,18 +4,21 @@
 //
 // A CTA owns 32 stacked rows and a range of their 16-token tiles, two of which
 // are in flight: the next tile's rows arrive (cp.async) while this one computes.
-//   S = Q . K^T    eight groups of 64 threads take an eighth of the 576-wide dot
-//                  each, 4 x 2 scores per thread; the parts are summed by the
+//   S = Q . K^T    sixteen groups of 16 threads take a sixteenth of the 576-wide
+//                  dot each, 8 x 4 scores per thread; the parts are summed by the
 //                  softmax.
-//   softmax        warp w keeps the online statistics of rows 2w and 2w+1, a lane
-//                  per token.
-//   O += P . V     thread = 8 rows x 4 columns of the 32 x 512 accumulator.
-// Both products are packed float32 FMAs (two per instruction: the plain ones
-// reach half the rate on sm_100) on 16-byte vectors of shared memory.
+//   softmax        warp w keeps the online statistics of rows 4w .. 4w+3, two at
+//                  a time, a lane per token.
+//   O += P . V     thread = 8 rows x 8 columns of the 32 x 512 accumulator.
+// Both products are packed float32 FMAs. What bounds them is what shared memory
+// returns to registers, 32 floats a clock and SM: S reads 24 floats for 64 FMA,
+// O 16 (tiles of 4 x 2 and 8 x 4 took 2.5 + 2.1 us a tile instead of 2.4 + 1.5).
 //
 // Tokens that no row may see are zeros in the tile, so whatever their cache
 // rows hold stays out of the sums; where a tile that some rows do not see holds
 // an infinity or NaN (its scores show it), the rows whose weight is 0 skip it.
+#include <algorithm>
+
 #include "once_per_device.h"
 #include "prefix.h"
 #include "sm100_ptx.cuh"
@@ -24,7 +27,7 @@ namespace mla {
 namespace {
 
 constexpr int kRows = 32, kToks = 16;
-constexpr int kThr = 512, kWarps = kThr / 32, kParts = kThr / 64;   // kParts slices of the dot product
+constexpr int kThr = 256, kWarps = kThr / 32, kParts = kThr / 16;   // kParts slices of the dot product
 constexpr int kPad = 4;             // floats of row padding: 16-byte rows, 8 rows over all banks
 constexpr int kPart = kToks + 1;
 
@@ -102,8 +105,8 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
   float* qs = smem;                              // [kRows][pitch]
   float* ks = qs + kRows * pitch;                // [2][kToks][pitch]
   float* part = ks + 2 * kToks * pitch;          // [kParts][kRows][kPart] parts of the scores
-  f32x2* ps = reinterpret_cast<f32x2*>(part + kParts * kRows * kPart);   // [kToks][kRows] weights, twice each
-  float* alpha = reinterpret_cast<float*>(ps + kToks * kRows);           // [kRows]
+  float* ps = part + kParts * kRows * kPart;     // [kToks][kRows] weights
+  float* alpha = ps + kToks * kRows;             // [kRows]
   float* stat = alpha + kRows;                   // [kRows] 1 / denominator
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -159,21 +162,27 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
   }
   copy_commit();
 
-  // S: thread (ty, tx) of part kq holds rows ty + 8i, tokens tx + 8n
-  const int kq = tid >> 6, ty = (tid >> 3) & 7, tx = tid & 7;
-  const int kq4 = D / (4 * kParts);              // float4 steps per part (D is a multiple of 32)
-  // softmax: row 2 warp + lane / 16, token lane % 16
+  // S: thread (ty, tx) of part kq holds rows ty + 4i, tokens tx + 4n
+  const int kq = tid >> 4, ty = (tid >> 2) & 3, tx = tid & 3;
+  const int kn = D / kParts;                     // channels per part, even (D is a multiple of 32)
+  // softmax: rows 4 warp + 2i + lane / 16, token lane % 16
   const int sub = lane >> 4, tok = lane & 15;
-  const int srow = 2 * warp + sub;
-  float m_run = -INFINITY, l_run = 0.f;
-  const int row_b = r0 + srow < p.N ? (r0 + srow) / p.HQ : -2;
-  int row_lim = 0x7fffffff;                      // last visible own token of the row
-  if (row_b >= 0 && p.causal) row_lim = prefix_len_of(p, row_b) - p.Q + (r0 + srow) % p.Q;
-  // O: rows 8 rg + i, columns 4 cg + k
-  const int rg = tid >> 7, cg = tid & 127;
-  f32x2 acc[8][2];
+  float m_run[2], l_run[2];
+  int row_b[2], row_lim[2];                      // sequence and last visible own token of the row
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = 0ull;
+  for (int i = 0; i < 2; ++i) {
+    m_run[i] = -INFINITY;
+    l_run[i] = 0.f;
+    const int r = r0 + 4 * warp + 2 * i + sub;
+    row_b[i] = r < p.N ? r / p.HQ : -2;
+    row_lim[i] = 0x7fffffff;
+    if (r < p.N && p.causal) row_lim[i] = prefix_len_of(p, row_b[i]) - p.Q + r % p.Q;
+  }
+  // O: rows 8 rg + i, columns 4 cg + k and 256 + 4 cg + k
+  const int rg = tid >> 6, cg = tid & 63;
+  f32x2 acc[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0ull;
 
   for (int j = j0; j < j1; ++j) {
     const int buf = (j - j0) & 1;
@@ -187,40 +196,39 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
     const bool pre = w.b < 0;
     bool odd = false;                            // a non-finite score: a non-finite key
     {
-      f32x2 s[4][2] = {};                          // sums over even and odd channels
-      const float* qp = qs + ty * pitch + 4 * kq * kq4;
-      const float* kp = kt + tx * pitch + 4 * kq * kq4;
-#pragma unroll 3
-      for (int k = 0; k < kq4; ++k) {
-        f32x4 qv[4], kv[2];
+      f32x2 s[8][4] = {};                          // sums over even and odd channels
+      const float* qp = qs + ty * pitch + kq * kn;
+      const float* kp = kt + tx * pitch + kq * kn;
+#pragma unroll 2
+      for (int k = 0; k < kn; k += 2) {
+        f32x2 qv[8], kv[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const f32x4*>(qp + 8 * i * pitch + 4 * k);
+        for (int i = 0; i < 8; ++i) qv[i] = *reinterpret_cast<const f32x2*>(qp + 4 * i * pitch + k);
 #pragma unroll
-        for (int n = 0; n < 2; ++n) kv[n] = *reinterpret_cast<const f32x4*>(kp + 8 * n * pitch + 4 * k);
+        for (int n = 0; n < 4; ++n) kv[n] = *reinterpret_cast<const f32x2*>(kp + 4 * n * pitch + k);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            fma2(s[i][n], qv[i].lo, kv[n].lo);
-            fma2(s[i][n], qv[i].hi, kv[n].hi);
-          }
+          for (int n = 0; n < 4; ++n) fma2(s[i][n], qv[i], kv[n]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < 4; ++n) {
           const float2 v = unpack2(s[i][n]);
-          part[(kq * kRows + ty + 8 * i) * kPart + tx + 8 * n] = v.x + v.y;
+          part[(kq * kRows + ty + 4 * i) * kPart + tx + 4 * n] = v.x + v.y;
           odd = odd || !isfinite(v.x + v.y);
         }
     }
     const bool any_odd = __syncthreads_or(odd);
-    {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int srow = 4 * warp + 2 * i + sub;
       const int t = w.t + tok;
       // own tokens are seen by their sequence's rows; a causal row sees own
       // tokens up to row_lim (a negative one reaches back into the prefix)
-      bool vis = row_lat[buf][tok] != nullptr && row_b >= 0 && (pre || row_b == w.b);
-      vis = vis && (!p.causal || (pre ? t - p.Lp : t) <= row_lim);
+      bool vis = row_lat[buf][tok] != nullptr && row_b[i] >= 0 && (pre || row_b[i] == w.b);
+      vis = vis && (!p.causal || (pre ? t - p.Lp : t) <= row_lim[i]);
       float s = 0.f;
 #pragma unroll
       for (int k = 0; k < kParts; ++k) s += part[(k * kRows + srow) * kPart + tok];
@@ -228,15 +236,15 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
       float mx = s;
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float m_new = fmaxf(m_run, mx);
-      const float al = m_run == -INFINITY ? 0.f : expf(m_run - m_new);
+      const float m_new = fmaxf(m_run[i], mx);
+      const float al = m_run[i] == -INFINITY ? 0.f : expf(m_run[i] - m_new);
       const float e = vis ? expf(s - m_new) : 0.f;
       float sum = e;
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      l_run = l_run * al + sum;
-      m_run = m_new;
-      ps[tok * kRows + srow] = pack2(e, e);
+      l_run[i] = l_run[i] * al + sum;
+      m_run[i] = m_new;
+      ps[tok * kRows + srow] = e;
       if (tok == 0) alpha[srow] = al;
     }
     __syncthreads();
@@ -245,31 +253,39 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
       const float al = alpha[8 * rg + i];
       const f32x2 al2 = pack2(al, al);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(acc[i][k]) : "l"(al2));
+      for (int k = 0; k < 4; ++k) asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(acc[i][k]) : "l"(al2));
     }
     if (!any_odd) {
 #pragma unroll 4
       for (int tt = 0; tt < kToks; ++tt) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 4 * cg);
+        const f32x4 v0 = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 4 * cg);
+        const f32x4 v1 = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 256 + 4 * cg);
+        const float4 pa = *reinterpret_cast<const float4*>(ps + tt * kRows + 8 * rg);
+        const float4 pb = *reinterpret_cast<const float4*>(ps + tt * kRows + 8 * rg + 4);
+        const float pr[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const f32x4 pr = *reinterpret_cast<const f32x4*>(ps + tt * kRows + 8 * rg + i);
-          fma2(acc[i][0], pr.lo, v.lo);
-          fma2(acc[i][1], pr.lo, v.hi);
-          fma2(acc[i + 1][0], pr.hi, v.lo);
-          fma2(acc[i + 1][1], pr.hi, v.hi);
+        for (int i = 0; i < 8; ++i) {
+          const f32x2 p2 = pack2(pr[i], pr[i]);
+          fma2(acc[i][0], p2, v0.lo);
+          fma2(acc[i][1], p2, v0.hi);
+          fma2(acc[i][2], p2, v1.lo);
+          fma2(acc[i][3], p2, v1.hi);
         }
       }
     } else {
 #pragma unroll 1
       for (int tt = 0; tt < kToks; ++tt) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 4 * cg);
+        const f32x4 v0 = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 4 * cg);
+        const f32x4 v1 = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 256 + 4 * cg);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const f32x2 pr = ps[tt * kRows + 8 * rg + i];
-          if (pr != 0ull) {
-            fma2(acc[i][0], pr, v.lo);
-            fma2(acc[i][1], pr, v.hi);
+          const float pr = ps[tt * kRows + 8 * rg + i];
+          if (pr != 0.f) {
+            const f32x2 p2 = pack2(pr, pr);
+            fma2(acc[i][0], p2, v0.lo);
+            fma2(acc[i][1], p2, v0.hi);
+            fma2(acc[i][2], p2, v1.lo);
+            fma2(acc[i][3], p2, v1.hi);
           }
         }
       }
@@ -281,9 +297,10 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
   // the rows' denominators to the accumulator's threads
   const bool split = p.num_splits > 1;
   __syncthreads();
-  {
-    float m = m_run, l = l_run;
-    const int r = r0 + srow;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float m = m_run[i], l = l_run[i];
+    const int r = r0 + 4 * warp + 2 * i + sub;
     float inv = 0.f;
     if (r < p.N) {
       float wt = 1.f;
@@ -311,16 +328,20 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
     const int r = r0 + 8 * rg + i;
     if (r >= p.N) continue;
     const float inv = stat[8 * rg + i];
-    const float2 lo = unpack2(acc[i][0]), hi = unpack2(acc[i][1]);
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (inv != 0.f) v = make_float4(lo.x * inv, lo.y * inv, hi.x * inv, hi.y * inv);
-    if (split)
-      *reinterpret_cast<float4*>(p.ws_o + ((int64_t)z * p.N + r) * p.Ckv + 4 * cg) = v;
-    else if constexpr (sizeof(T) == 4)
-      *reinterpret_cast<float4*>(reinterpret_cast<T*>(p.x) + (int64_t)r * p.Ckv + 4 * cg) = v;
-    else
-      *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.x) + (int64_t)r * p.Ckv + 4 * cg) =
-          make_uint2(sm100::pack_bf16(v.x, v.y), sm100::pack_bf16(v.z, v.w));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = 256 * k + 4 * cg;
+      const float2 lo = unpack2(acc[i][2 * k]), hi = unpack2(acc[i][2 * k + 1]);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (inv != 0.f) v = make_float4(lo.x * inv, lo.y * inv, hi.x * inv, hi.y * inv);
+      if (split)
+        *reinterpret_cast<float4*>(p.ws_o + ((int64_t)z * p.N + r) * p.Ckv + c) = v;
+      else if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4*>(reinterpret_cast<T*>(p.x) + (int64_t)r * p.Ckv + c) = v;
+      else
+        *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.x) + (int64_t)r * p.Ckv + c) =
+            make_uint2(sm100::pack_bf16(v.x, v.y), sm100::pack_bf16(v.z, v.w));
+    }
   }
 }
 
@@ -349,17 +370,19 @@ cudaError_t launch(const PrefixParams& p, cudaStream_t st) {
 }  // namespace
 
 size_t prefix_simt_smem(int D) {
-  return sizeof(float) * ((size_t)(kRows + 2 * kToks) * pitch_of(D) + kParts * kRows * kPart + 2 * kToks * kRows + 2 * kRows);
+  return sizeof(float) * ((size_t)(kRows + 2 * kToks) * pitch_of(D) + kParts * kRows * kPart + kToks * kRows + 2 * kRows);
 }
 
-// about one CTA per SM (its shared memory fills one), at least four tiles each:
-// a split costs a merge of about 3 us, a tile takes 2.2
+// About one CTA per SM (its shared memory fills one), no split shorter than a
+// tile: a tile takes 5.4 us, the merge of a few splits 3.
 int prefix_simt_auto_splits(const mla_prefix_args* a, int sms) {
-  const int64_t rows = (int64_t)a->B * a->H * a->Q;
+  const int HQ = a->H * a->Q;
+  const int64_t rows = (int64_t)a->B * HQ;
   const int64_t blocks = (rows + kRows - 1) / kRows;
-  const int64_t tiles = ((int64_t)a->prefix_len + kToks - 1) / kToks + (a->Lk + kToks - 1) / kToks;
+  const int64_t seqs = std::min<int64_t>(a->B, (kRows + HQ - 1) / HQ);   // of a block
+  const int64_t tiles = ((int64_t)a->prefix_len + kToks - 1) / kToks + seqs * ((a->Lk + kToks - 1) / kToks);
   int64_t s = sms / blocks;
-  if (s > tiles / 4) s = tiles / 4;
+  if (s > tiles) s = tiles;
   if (s > 64) s = 64;
   return s < 1 ? 1 : (int)s;
 }
