@@ -424,7 +424,7 @@ mla_status_t mla_rope_append(const mla_rope_append_args* a, void* stream);
  *     anything, NaN included.
  *   sinks: as for mla_decode.
  *   Supported: MLA_F32 or MLA_BF16; Ckv = 512; Dr 0, 32 or 64; H a multiple of 8
- *     up to 128, Q 1..4. bf16 with contiguous storage or pages of a
+ *     up to 128, Q 1..4; B*H*Q up to 2^24, prefix_len + Lk up to 2^30. bf16 with contiguous storage or pages of a
  *     multiple of 64 rows runs on the tensor cores; everything else in float32
  *     on the CUDA cores.
  *   num_splits: 0 = auto; each block of stacked rows cuts its tokens into this

@@ -461,8 +461,8 @@ mla_status_t validate_prefix(const mla_prefix_args* a) {
   if (a->dtype != MLA_F32 && a->dtype != MLA_BF16) return MLA_ERR_UNSUPPORTED;
   if (a->Ckv != mla::kCkv || !(a->Dr == 0 || a->Dr == 32 || a->Dr == 64)) return MLA_ERR_UNSUPPORTED;
   if (a->H < 8 || a->H > 128 || a->H % 8 != 0 || a->Q > 4) return MLA_ERR_UNSUPPORTED;
-  // stacked rows and positions are 32-bit
-  if ((int64_t)a->B * a->H * a->Q > (1 << 30) || (int64_t)a->prefix_len + a->Lk > (1 << 30))
+  // stacked rows (times splits) and positions are 32-bit
+  if ((int64_t)a->B * a->H * a->Q > (1 << 24) || (int64_t)a->prefix_len + a->Lk > (1 << 30))
     return MLA_ERR_UNSUPPORTED;
   if (a->num_splits < 0 || a->num_splits > kMaxSplits) return MLA_ERR_INVALID_ARG;
   if (!a->q_lat || !a->x || (a->Dr > 0 && !a->q_pe)) return MLA_ERR_INVALID_ARG;

@@ -213,16 +213,16 @@ __device__ __forceinline__ Block64 block64(const PrefixParams& p, const TileWalk
 // heads, a 16384-token paged prefix).
 __device__ __forceinline__ bool bad_pages(const PrefixParams& p, int b0, int b1, int j0, int nt, int tid, int n) {
   bool bad = false;
-  const int ps = p.page_size;
+  const int64_t ps = p.page_size;
   if (p.ptable) {
     const int end = min(p.Lp, (j0 + nt) * kTileT);
-    for (int i = j0 * kTileT / ps + tid; i * ps < end; i += n) bad = bad || p.ptable[i] < 0 || p.ptable[i] >= p.p_pages;
+    for (int64_t i = j0 * kTileT / ps + tid; i * ps < end; i += n) bad = bad || p.ptable[i] < 0 || p.ptable[i] >= p.p_pages;
   }
   if (p.table)
     for (int b = b0; b <= b1; ++b) {
       const int32_t* t = p.table + (int64_t)b * p.max_pages;
       const int len = prefix_len_of(p, b);
-      for (int i = tid; i * ps < len; i += n) bad = bad || t[i] < 0 || t[i] >= p.num_pages;
+      for (int64_t i = tid; i * ps < len; i += n) bad = bad || t[i] < 0 || t[i] >= p.num_pages;
     }
   return bad;
 }

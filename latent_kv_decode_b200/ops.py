@@ -512,6 +512,13 @@ def _int32(t: torch.Tensor, name: str) -> int:
     return t.data_ptr()
 
 
+def _int_range(*vs) -> None:
+    """The arguments fit the C ABI's int (ctypes would cut them silently)."""
+    for v in vs:
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise MlaError(f"{v} is beyond 32 bits")
+
+
 def _launch(fn, dev: int, stream, *made):
     """Call ``fn(stream handle)`` with device ``dev`` current, on ``stream`` or that
     device's current stream; memory ``made`` for the call is tied to a stream
@@ -534,6 +541,8 @@ def _launch(fn, dev: int, stream, *made):
 def _cache_rows(kv_cache, pe_cache, block_table, page_size: int, Lk: Optional[int], B: int, Ckv: int, Dr: int):
     """(kv row stride, pe row stride, kv batch stride, pe batch stride, Lk, table, max_pages, num_pages) of
     (B, Lk, C) views, or of (num_pages, page_size, C) pools with a (B, max_pages) ``block_table``."""
+    if kv_cache.dim() != 3:
+        raise MlaError("kv_cache must be 3-D")
     n0, n1, width = kv_cache.shape
     kb, kr, k1 = kv_cache.stride()
     pb = pr = 0
@@ -555,12 +564,17 @@ def _cache_rows(kv_cache, pe_cache, block_table, page_size: int, Lk: Optional[in
             raise MlaError("Lk is beyond the cache's rows")
         return kr, pr, kb, pb, Lk, None, 0, 0
     table = _int32(block_table, "block_table")
+    if block_table.dim() != 2:
+        raise MlaError("block_table must be (B, max_pages)")
     rows, max_pages = block_table.shape
     if rows != B or n1 != page_size:
         raise MlaError("block_table must be (B, max_pages), and the pool's pages of page_size rows")
     if n0 > 1 and (kb != n1 * kr or (Dr and pb != n1 * pr)):
         raise MlaError("a pool's pages must follow each other")
-    return kr, pr, 0, 0, max_pages * page_size if Lk is None else Lk, table, max_pages, n0
+    if Lk is None:
+        Lk = max_pages * page_size
+    _int_range(Lk)
+    return kr, pr, 0, 0, Lk, table, max_pages, n0
 
 
 def _step(t: torch.Tensor, uniform: bool) -> int:
@@ -627,6 +641,7 @@ def make_rope_append_args(c_kv, k_pe, kv_cache, pe_cache, seq_lens, *, q_pe=None
         raise MlaError("mla_rope_append: q_out without q_pe")
     kr, pr, kb, pb, Lk, table, max_pages, num_pages = _cache_rows(kv_cache, pe_cache, block_table, page_size, Lk, B,
                                                                   Ckv, Dr)
+    _int_range(N, pos_offset)
     a = RopeAppendArgs(B, Q, N, Ckv, Dr, H, _qdtype(c_kv), c_kv.data_ptr(), k_pe.data_ptr(), qp, op,
                        _step(c_kv, uniform), _step(k_pe, uniform), qs, qh, ob, ot, oh, kv_cache.data_ptr(),
                        pe_cache.data_ptr(), kr, pr, kb, pb, Lk, _int32(seq_lens, "seq_lens"), table, max_pages,
@@ -683,6 +698,8 @@ def make_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, so
     for t in (q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, x):
         if t is not None and t.dtype is not dtype:
             raise MlaError("mla_prefix_decode: tensors must share one dtype")
+    if q_lat.dim() != 4:
+        raise MlaError("q_lat must be (B, H, Q, 512)")
     B, H, Q, Ckv = shape = q_lat.shape
     Dr, qp = 0, None
     if q_pe is not None:
@@ -732,6 +749,7 @@ def make_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, so
     elif Lk:
         raise MlaError("Lk without kv_cache")
     Lk = Lk or 0
+    _int_range(prefix_len, Lk, num_splits)
     lens = None
     if seq_lens is not None:
         lens = _int32(seq_lens, "seq_lens")
@@ -868,7 +886,7 @@ def _fp4_linear(x, w, dims, strides, scale: float, out, err_flag, stream):
 def mla_fp4_linear(x: torch.Tensor, w: torch.Tensor, scale: float = 1.0, *, out: Optional[torch.Tensor] = None,
                    err_flag=None, stream=None) -> torch.Tensor:
     """out[..., n] = scale * sum_k x[..., k] W[n, k]: x (..., K) bf16, w (N, K/512, 288) FP4 entries."""
-    *lead, K = x.shape
+    *lead, K = x.shape if x.dim() else (0,)
     if w.dim() != 3 or K != w.shape[1] * FP4_BLOCK:
         raise MlaError("mla_fp4_linear: w must be (N, K/512, 288) for x (..., K)")
     N = w.shape[0]
