@@ -431,7 +431,8 @@ mla_status_t mla_rope_append(const mla_rope_append_args* a, void* stream);
  *     many ranges, and the call then merges the partial results itself (no
  *     mla_combine): x and lse are final when the enqueued work completes.
  *   workspace: mla_prefix_decode_workspace_size(a) bytes, 256-byte aligned
- *     (may be NULL when that is 0). It is written before it is read in every call.
+ *     (may be NULL when that is 0). It is written before it is read in every call;
+ *     calls whose GPU work overlaps in time need one each.
  *   err_flag: as for mla_decode.
  */
 typedef struct mla_prefix_args {
@@ -483,9 +484,11 @@ mla_status_t mla_prefix_decode(const mla_prefix_args* a, void* workspace, size_t
  *       strides in elements, multiples of 8 (x (B,H,Q,512) with H/G heads per
  *       group: strides H*Q*512, 512, (H/G)*Q*512, Q*512).
  *   out (B*Q, G*N) bf16, packed. Products and sums are float32, rounded once.
- *   K a multiple of 512; any B, Q, G, N. x and w 16-byte aligned.
+ *   K a multiple of 512; B*Q up to 2^20, G up to 65535, G*N up to 2^30. x and w
+ *       16-byte aligned.
  *   workspace: mla_fp4_linear_workspace_size(a) bytes, 256-byte aligned (may
- *       be NULL when that is 0). It is written before it is read in every call.
+ *       be NULL when that is 0). It is written before it is read in every call;
+ *       calls whose GPU work overlaps in time need one each.
  *   err_flag: optional device int32; MLA_DEVICE_ERR_TIMEOUT when a bounded wait
  *       inside the kernel gave up (the output is then not valid).
  */

@@ -408,7 +408,7 @@ namespace {
 mla_status_t validate_rope_append(const mla_rope_append_args* a) {
   if (!a) return MLA_ERR_INVALID_ARG;
   if (a->B <= 0 || a->N < 0 || a->Lk <= 0 || a->Ckv <= 0 || a->Dr <= 0 || a->H < 0) return MLA_ERR_INVALID_ARG;
-  if (!a->cu_tokens && (a->Q <= 0 || (int64_t)a->B * a->Q != a->N)) return MLA_ERR_INVALID_ARG;
+  if (!a->cu_tokens && (a->Q < 0 || (int64_t)a->B * a->Q != a->N)) return MLA_ERR_INVALID_ARG;
   if (a->dtype != MLA_F32 && a->dtype != MLA_BF16) return MLA_ERR_UNSUPPORTED;
   if (a->Ckv != mla::kCkv || (a->Dr != 32 && a->Dr != 64) || a->H > 1024) return MLA_ERR_UNSUPPORTED;
   if (!(a->rope_theta > 0.f) || !isfinite(a->rope_theta)) return MLA_ERR_INVALID_ARG;
@@ -594,8 +594,8 @@ mla_status_t validate_fp4_linear(const mla_fp4_linear_args* a) {
   for (int64_t s : {a->x_batch_stride, a->x_token_stride, a->x_group_stride, a->x_block_stride})
     if (s < 0 || s % 8 != 0) return MLA_ERR_INVALID_ARG;
   if (a->K % mla::kCkv != 0) return MLA_ERR_UNSUPPORTED;
-  // tokens and rows are 32-bit, and a grid dimension holds the token blocks
-  if ((int64_t)a->B * a->Q > 65535 * 8 || (int64_t)a->G * a->N > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+  // tokens and rows are 32-bit, and a grid dimension holds the groups
+  if ((int64_t)a->B * a->Q > (1 << 20) || (int64_t)a->G * a->N > (1 << 30) || a->G > 65535) return MLA_ERR_UNSUPPORTED;
   return MLA_OK;
 }
 

@@ -538,6 +538,22 @@ def _launch(fn, dev: int, stream, *made):
     return r
 
 
+class _copies_on:
+    """Copies that a call makes of its inputs run on the call's stream, whose
+    earlier work may still be writing them."""
+
+    def __init__(self, dev: int, stream):
+        self._in = None if stream is None else torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=dev))
+
+    def __enter__(self):
+        if self._in is not None:
+            self._in.__enter__()
+
+    def __exit__(self, *exc):
+        if self._in is not None:
+            self._in.__exit__(*exc)
+
+
 def _cache_rows(kv_cache, pe_cache, block_table, page_size: int, Lk: Optional[int], B: int, Ckv: int, Dr: int):
     """(kv row stride, pe row stride, kv batch stride, pe batch stride, Lk, table, max_pages, num_pages) of
     (B, Lk, C) views, or of (num_pages, page_size, C) pools with a (B, max_pages) ``block_table``."""
@@ -585,7 +601,7 @@ def _step(t: torch.Tensor, uniform: bool) -> int:
     if not uniform:
         return st[0]
     B, Q = t.shape[:2]
-    if Q == 1:
+    if Q <= 1:
         return st[0]
     if B > 1 and st[0] != Q * st[1]:
         raise MlaError("mla_rope_append: tokens must step evenly")
@@ -628,7 +644,7 @@ def make_rope_append_args(c_kv, k_pe, kv_cache, pe_cache, seq_lens, *, q_pe=None
             raise MlaError("mla_rope_append: q_pe must hold the tokens' heads, Dr wide")
         shape = (B, H, Q, Dr) if uniform else (N, H, Dr)
         if q_out is None:
-            q_out = torch.empty(shape, dtype=dtype, device=q_pe.device)
+            q_out = q_pe.new_empty(shape)
         elif tuple(q_out.shape) != shape or q_out.stride(-1) != 1:
             raise MlaError(f"mla_rope_append: q_out must be {shape}, last dim packed")
         qs, qh = _step(q_pe, uniform), q_pe.stride(-2)
@@ -689,7 +705,8 @@ def make_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, so
     prefix_kv / prefix_pe: (prefix_len, C) rows, or (pages, page_size, C) pools
     with ``prefix_table`` and ``prefix_len``; None with ``prefix_len`` 0.
     kv_cache / pe_cache: the sequences' own tokens, laid out as for mla_decode,
-    or None (no own tokens). ``causal_mask`` covers prefix_len + Lk positions.
+    or None (no own tokens). ``causal_mask`` (uint8 or bool, contiguous) covers
+    prefix_len + Lk positions.
     """
     dev = q_lat.get_device()
     _same_device(dev, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, prefix_table, seq_lens, block_table,
@@ -757,21 +774,22 @@ def make_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, so
             raise MlaError("seq_lens must have B elements")
     mask = None
     if causal_mask is not None:
-        causal_mask = causal_mask.reshape(-1).to(torch.uint8).contiguous()
+        if causal_mask.dtype not in (torch.uint8, torch.bool) or not causal_mask.is_contiguous():
+            raise MlaError("causal_mask must be contiguous uint8 or bool")
         mask = causal_mask.data_ptr()
         if causal_mask.numel() < prefix_len + Lk:
             raise MlaError("causal_mask must cover prefix_len + Lk positions")
     if sinks is not None and (sinks.dtype is not torch.float32 or not sinks.is_contiguous() or sinks.numel() != H):
         raise MlaError("sinks must be (H) float32")
     if x is None:
-        x = torch.empty(shape, dtype=dtype, device=q_lat.device)
+        x = torch.empty_like(q_lat)
     elif not x.is_contiguous() or x.shape != shape:
         raise MlaError("x must be contiguous (B, H, Q, 512)")
     if lse is not None:
         if lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() != B * H * Q:
             raise MlaError("lse must be contiguous float32 (B, H, Q)")
     elif want_lse:
-        lse = torch.empty((B, H, Q), dtype=torch.float32, device=q_lat.device)
+        lse = q_lat.new_empty((B, H, Q), dtype=torch.float32)
     a = PrefixArgs(B, H, Q, Ckv, Dr, _qdtype(q_lat), q_lat.data_ptr(), qp, pk, pp, pks, pps, prefix_len, ptab, p_pages,
                    k, p, kr, pr, kb, pb, Lk, lens, table, max_pages, page_size, num_pages, mask, bool(causal),
                    softmax_scale, _ptr(sinks), num_splits, x.data_ptr(), _ptr(lse),
@@ -810,9 +828,15 @@ def mla_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, sof
                       stream=None, **kw):
     """Decode of a batch that shares a prefix; returns (x, lse), final when the enqueued work completes.
 
-    Arguments as in :func:`make_prefix_decode`. The call merges its split
-    partials itself: there is no combine to call after it.
+    Arguments as in :func:`make_prefix_decode`; ``causal_mask`` may have any dtype
+    (0 = hidden). The call merges its split partials itself: there is no combine
+    to call after it.
     """
+    mask = kw.get("causal_mask")
+    if mask is not None and (mask.dtype not in (torch.uint8, torch.bool) or not mask.is_contiguous()):
+        _same_device(q_lat.get_device(), mask)
+        with _copies_on(q_lat.get_device(), stream):
+            kw["causal_mask"] = mask.ne(0).contiguous()
     return launch_prefix_decode(make_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache,
                                                    softmax_scale, **kw), stream=stream)
 
@@ -890,13 +914,16 @@ def mla_fp4_linear(x: torch.Tensor, w: torch.Tensor, scale: float = 1.0, *, out:
     if w.dim() != 3 or K != w.shape[1] * FP4_BLOCK:
         raise MlaError("mla_fp4_linear: w must be (N, K/512, 288) for x (..., K)")
     N = w.shape[0]
-    x2 = x if len(lead) == 1 else x.reshape(-1, K)
-    step, one = x2.stride()
-    if one != 1 or step % 8 or x2.data_ptr() % 16:
-        x2 = x2.contiguous()
-        step = K
+    x2 = x
+    if len(lead) != 1 or x.stride(1) != 1 or x.stride(0) % 8 or x.data_ptr() % 16:
+        _same_device(x.get_device())
+        with _copies_on(x.get_device(), stream):
+            x2 = x.contiguous().view(-1, K)
+            if x2.data_ptr() % 16:
+                x2 = x2.clone()
+    step = x2.stride(0)
     if out is None:
-        out = torch.empty((*lead, N), dtype=torch.bfloat16, device=x.device)
+        out = x.new_empty((*lead, N), dtype=torch.bfloat16)
     elif list(out.shape) != [*lead, N]:
         raise MlaError("mla_fp4_linear: out has another shape")
     return _fp4_linear(x2, w, (x2.shape[0], 1, 1, N, K), (step, 0, 0, FP4_BLOCK), scale, out, err_flag, stream)
@@ -918,11 +945,13 @@ def mla_fp4_group_wo(x: torch.Tensor, wo_a: torch.Tensor, wo_b: Optional[torch.T
         raise MlaError("mla_fp4_group_wo: wo_a must be (G, R, H/G, 288)")
     sb, sh, sq, one = x.stride()
     if one != 1 or sb % 8 or sh % 8 or sq % 8 or x.data_ptr() % 16:
-        x = x.contiguous()
+        _same_device(x.get_device())
+        with _copies_on(x.get_device(), stream):
+            x = x.clone(memory_format=torch.contiguous_format)
         sb, sh, sq, one = x.stride()
     z = out if wo_b is None else None
     if z is None:
-        z = torch.empty((B, Q, G * R), dtype=torch.bfloat16, device=x.device)
+        z = x.new_empty((B, Q, G * R), dtype=torch.bfloat16)
     elif tuple(z.shape) != (B, Q, G * R):
         raise MlaError("mla_fp4_group_wo: out has another shape")
     _fp4_linear(x, wo_a, (B, Q, G, R, per * FP4_BLOCK), (sb, sq, per * sh, sh), scale_a, z, err_flag, stream)

@@ -150,6 +150,7 @@ def _linear(**over):
     (dict(N=0), 1), (dict(K=0), 1), (dict(K=768), 2), (dict(x=FAKE + 8), 1), (dict(w=FAKE + 8), 1), (dict(out=FAKE + 1), 1),
     (dict(x_batch_stride=12), 1), (dict(x_token_stride=-512), 1), (dict(x_block_stride=4), 1), (dict(err_flag=FAKE + 2), 1),
     (dict(scale=float("inf")), 1), (dict(scale=float("nan")), 1), (dict(B=1 << 20), 2), (dict(N=1 << 29), 2),
+    (dict(G=70000, N=1), 2),
 ])
 def test_fp4_linear_rejects(L, over, status):
     a = _linear(**over)

@@ -159,6 +159,36 @@ def test_equal_results_on_repeat_and_on_another_stream():
     assert all(torch.equal(o, y) for o in out)
 
 
+def test_inputs_that_need_a_copy():
+    """Activations the kernel cannot read in place: copied, on the call's own stream."""
+    from latent_kv_decode_b200 import ops
+    w = _entries((70, 2), seed=12).cuda()
+    x = torch.randn(4, 3, 1024, generator=torch.Generator().manual_seed(13)).bfloat16().cuda()
+    want = ops.mla_fp4_linear(x, w)
+    assert want.shape == (4, 3, 70)
+    odd = torch.zeros((4, 3, 1027), dtype=torch.bfloat16, device="cuda")
+    odd[..., 1:1025] = x
+    back = x.transpose(0, 1).contiguous().transpose(0, 1)
+    packed_off = torch.cat([x.new_zeros(1), x.flatten()])[1:].view(4, 3, 1024)      # contiguous, 2 bytes off
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for v in (odd[..., 1:1025], back, packed_off, x[0, 0]):
+        for stream in (None, s):
+            y = ops.mla_fp4_linear(v, w, stream=stream)
+            s.synchronize()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want if v.dim() == 3 else want[0, 0])
+    wg = _entries((2, 70, 1), seed=14).cuda()
+    x4 = torch.randn(2, 2, 3, 512, generator=torch.Generator().manual_seed(15)).bfloat16().cuda()
+    want = ops.mla_fp4_group_wo(x4, wg)
+    odd = torch.zeros((2, 2, 3, 515), dtype=torch.bfloat16, device="cuda")
+    odd[..., 3:] = x4
+    torch.cuda.synchronize()
+    y = ops.mla_fp4_group_wo(odd[..., 3:], wg, stream=s)
+    s.synchronize()
+    assert torch.equal(y, want)
+
+
 def test_no_tokens_and_refusals():
     from latent_kv_decode_b200 import ops
     w = _entries((8, 1), seed=11).cuda()

@@ -208,6 +208,20 @@ def test_equal_results_captured_and_on_another_stream():
     assert torch.equal(rows.cpu(), want[0]) and torch.equal(out.cpu(), want[1])
 
 
+def test_no_tokens():
+    from latent_kv_decode_b200 import ops
+    d = _case([1, 1], [3, 4], 8, 64, torch.bfloat16, 0, seed=10)
+    rows, kv_a, q = d["rows"].cuda(), d["kv_a"].cuda(), d["q"].cuda()
+    lens = torch.tensor(d["lens"], dtype=torch.int32).cuda()
+    out = ops.mla_rope_append(kv_a[:0, None, :C].expand(0, 1, C).reshape(2, 0, C), kv_a[:0, C:C + 64].reshape(2, 0, 64),
+                              rows[..., :C], rows[..., C:], lens, q_pe=q[:0, :, 128:].reshape(2, 0, 8, 64))
+    assert out.shape == (2, 8, 0, 64)
+    out = ops.mla_rope_append(kv_a[:0, :C], kv_a[:0, C:C + 64], rows[..., :C], rows[..., C:], lens, q_pe=q[:0, :, 128:],
+                              cu_tokens=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert out.shape == (0, 8, 64) and torch.equal(rows.cpu(), d["rows"])
+
+
 def test_refusals():
     from latent_kv_decode_b200 import ops
     d = _case([2, 2], [0, 9], 8, 64, torch.bfloat16, 64, seed=9)

@@ -173,6 +173,25 @@ def test_two_streams_at_once_and_workspaces():
             assert torch.equal(x, want[k][0]) and torch.equal(lse, want[k][1])
 
 
+def test_masks_of_any_type():
+    from latent_kv_decode_b200 import ops
+    g = torch.Generator("cuda").manual_seed(5)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    q, qp, p, own = r(2, 16, 1, C), r(2, 16, 1, DR), r(100, C + DR), r(2, 40, C + DR)
+    mask = torch.rand(140, generator=g, device="cuda") < 0.5
+    call = lambda m, **kw: ops.mla_prefix_decode(q, qp, p[:, :C], p[:, C:], own[..., :C], own[..., C:], 0.07, causal_mask=m, **kw)
+    want = call(mask)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for m in (mask.to(torch.uint8), mask.float() * 0.25, mask.long().reshape(1, 1, 1, -1), torch.stack([mask, mask], 1)[:, 0]):
+        for kw in ({}, dict(stream=s)):
+            x, lse = call(m, **kw)
+            torch.cuda.synchronize()
+            assert torch.equal(x, want[0]) and torch.equal(lse, want[1])
+    with pytest.raises(ops.MlaError):
+        ops.make_prefix_decode(q, qp, p[:, :C], p[:, C:], own[..., :C], own[..., C:], 0.07, causal_mask=mask.float())
+
+
 def test_refusals_of_the_prefix_decode():
     from latent_kv_decode_b200 import ops
     z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt, device="cuda")
