@@ -1,10 +1,12 @@
-"""Build libmla.so in-tree with nvcc for sm_100a.
+"""Build libmla.so in-tree with nvcc for sm_100a, and the binding module _step beside it.
 
     python -m latent_kv_decode_b200.build            # incremental
     python -m latent_kv_decode_b200.build --force    # rebuild everything
 
 Each ``csrc/*.cu`` compiles to ``_build/*.o`` (only when the source or a
 header is newer), then everything links into ``latent_kv_decode_b200/libmla.so``.
+``csrc/step_binding.cpp`` (torch's C++ headers, the host compiler) becomes
+``latent_kv_decode_b200/_step.so``, linked against that library.
 Needs no GPU: nvcc cross-compiles for the B200.
 """
 from __future__ import annotations
@@ -15,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +25,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmla.so")
+STEP_SRC = os.path.join(CSRC, "step_binding.cpp")
+STEP = os.path.join(PKG, "_step.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -55,7 +60,7 @@ def _compile(src: str, force: bool, verbose: bool) -> str:
     return obj
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
+def build(force: bool = False, verbose: bool = False, build_binding: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
@@ -67,7 +72,33 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    if build_binding:
+        build_step(force, verbose)
     return LIB
+
+
+def build_step(force: bool = False, verbose: bool = False) -> str:
+    """The C++ binding of the serving-step calls (needs libmla.so)."""
+    header = os.path.join(ROOT, "include", "mla.h")
+    newest = max(os.path.getmtime(STEP_SRC), os.path.getmtime(header))
+    if not force and os.path.exists(STEP) and os.path.getmtime(STEP) >= newest:
+        return STEP
+    import torch
+    tdir = os.path.dirname(os.path.abspath(torch.__file__))
+    inc = [os.path.join(tdir, "include"), os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    tmp = STEP + ".tmp"
+    cmd = ([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [x for d in inc for x in ("-isystem", d)] +
+           [STEP_SRC, "-o", tmp, "-L" + PKG, "-l:" + os.path.basename(LIB), "-L" + os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+            "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + os.path.join(tdir, "lib")])
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {STEP_SRC}:\n{r.stdout}\n{r.stderr}")
+    if verbose:
+        sys.stderr.write(r.stderr)
+    os.replace(tmp, STEP)
+    return STEP
 
 
 if __name__ == "__main__":

@@ -1,4 +1,4 @@
-"""ctypes binding of libmla.so (include/mla.h): argument marshalling only.
+"""Binding of libmla.so (include/mla.h): argument marshalling only.
 
 Every function takes torch CUDA tensors, passes their device pointers,
 strides and the current CUDA stream to the C ABI, and raises on a non-zero
@@ -33,6 +33,7 @@ Calls (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from dataclasses import dataclass, field
 from typing import Optional
@@ -494,369 +495,107 @@ def mla_group_wo(x, wo_a, wo_b=None, *, stream=None, **kw) -> torch.Tensor:
 
 # --- the step on raw projection outputs, shared prefixes and FP4 weights -----
 #
-# These calls are small next to the GPU's work only while the host stays out of
-# the way, so their checks read each tensor property once.
+# At a decode step's sizes the GPU needs these calls for a few microseconds, so
+# their marshalling is C++ (csrc/step_binding.cpp, module _step): it checks the
+# tensors, allocates outputs and workspace, and calls libmla.so on ``stream``
+# (default: the current stream of the tensors' device).
 
-def _same_device(dev: int, *ts) -> None:
-    if dev < 0:
-        raise MlaError("libmla takes CUDA tensors only")
-    for t in ts:
-        if t is not None and t.get_device() != dev:
-            raise MlaError("libmla takes CUDA tensors of one device")
+STEP_PATH = os.path.join(_HERE, "_step.so")
+_step_mod = None
 
 
-def _int32(t: torch.Tensor, name: str) -> int:
-    """Device pointer of a contiguous int32 tensor."""
-    if t.dtype is not torch.int32 or not t.is_contiguous():
-        raise MlaError(f"{name} must be contiguous int32")
-    return t.data_ptr()
+def _step():
+    """Load the binding module _step.so once; raise if it is not built."""
+    global _step_mod
+    if _step_mod is None:
+        lib()
+        if not os.path.exists(STEP_PATH):
+            raise MlaError(f"{STEP_PATH} is missing; build it with `python -m latent_kv_decode_b200.build`")
+        spec = importlib.util.spec_from_file_location("_step", STEP_PATH)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.set_error(MlaError)
+        _step_mod = mod
+    return _step_mod
 
 
-def _int_range(*vs) -> None:
-    """The arguments fit the C ABI's int (ctypes would cut them silently)."""
-    for v in vs:
-        if not -2 ** 31 <= v < 2 ** 31:
-            raise MlaError(f"{v} is beyond 32 bits")
-
-
-def _launch(fn, dev: int, stream, *made):
-    """Call ``fn(stream handle)`` with device ``dev`` current, on ``stream`` or that
-    device's current stream; memory ``made`` for the call is tied to a stream
-    that is not the current one."""
-    current = torch._C._cuda_getCurrentRawStream(dev)
-    handle = current if stream is None else _stream(stream)
-    if torch.cuda.current_device() == dev:
-        r = fn(handle)
-    else:
-        with torch.cuda.device(dev):
-            r = fn(handle)
-    if handle != current:
-        s = torch.cuda.ExternalStream(handle, device=dev)
-        for t in made:
-            if t is not None:
-                t.record_stream(s)
-    return r
-
-
-class _copies_on:
-    """Copies that a call makes of its inputs run on the call's stream, whose
-    earlier work may still be writing them."""
-
-    def __init__(self, dev: int, stream):
-        self._in = None if stream is None else torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=dev))
-
-    def __enter__(self):
-        if self._in is not None:
-            self._in.__enter__()
-
-    def __exit__(self, *exc):
-        if self._in is not None:
-            self._in.__exit__(*exc)
-
-
-def _cache_rows(kv_cache, pe_cache, block_table, page_size: int, Lk: Optional[int], B: int, Ckv: int, Dr: int):
-    """(kv row stride, pe row stride, kv batch stride, pe batch stride, Lk, table, max_pages, num_pages) of
-    (B, Lk, C) views, or of (num_pages, page_size, C) pools with a (B, max_pages) ``block_table``."""
-    if kv_cache.dim() != 3:
-        raise MlaError("kv_cache must be 3-D")
-    n0, n1, width = kv_cache.shape
-    kb, kr, k1 = kv_cache.stride()
-    pb = pr = 0
-    if Dr:
-        if pe_cache is None or pe_cache.dim() != 3:
-            raise MlaError("pe_cache must be 3-D")
-        m0, m1, pwidth = pe_cache.shape
-        pb, pr, p1 = pe_cache.stride()
-        if m0 != n0 or m1 != n1 or pwidth < Dr or p1 != 1:
-            raise MlaError("pe_cache must hold kv_cache's rows, at least Dr wide, last dim packed")
-    if width < Ckv or k1 != 1:
-        raise MlaError("kv_cache rows must be at least 512 wide, last dim packed")
-    if block_table is None:
-        if n0 != B:
-            raise MlaError("a contiguous cache must be (B, Lk, C)")
-        if Lk is None:
-            Lk = n1
-        elif Lk > n1:
-            raise MlaError("Lk is beyond the cache's rows")
-        return kr, pr, kb, pb, Lk, None, 0, 0
-    table = _int32(block_table, "block_table")
-    if block_table.dim() != 2:
-        raise MlaError("block_table must be (B, max_pages)")
-    rows, max_pages = block_table.shape
-    if rows != B or n1 != page_size:
-        raise MlaError("block_table must be (B, max_pages), and the pool's pages of page_size rows")
-    if n0 > 1 and (kb != n1 * kr or (Dr and pb != n1 * pr)):
-        raise MlaError("a pool's pages must follow each other")
-    if Lk is None:
-        Lk = max_pages * page_size
-    _int_range(Lk)
-    return kr, pr, 0, 0, Lk, table, max_pages, n0
-
-
-def _step(t: torch.Tensor, uniform: bool) -> int:
-    """Stride from token to token of (N, ...) or (B, Q, ...) rows with a packed last dim."""
-    st = t.stride()
-    if st[-1] != 1:
-        raise MlaError("mla_rope_append: the last dim must be packed")
-    if not uniform:
-        return st[0]
-    B, Q = t.shape[:2]
-    if Q <= 1:
-        return st[0]
-    if B > 1 and st[0] != Q * st[1]:
-        raise MlaError("mla_rope_append: tokens must step evenly")
-    return st[1]
-
-
-def make_rope_append_args(c_kv, k_pe, kv_cache, pe_cache, seq_lens, *, q_pe=None, q_out=None, cu_tokens=None,
-                          block_table=None, page_size: int = 64, pos_offset: int = 0,
-                          rope_theta: float = 10000.0, err_flag=None, Lk: Optional[int] = None):
-    """Fill a RopeAppendArgs from tensors (no GPU work); returns (args, q_out).
+def mla_rope_append(c_kv, k_pe, kv_cache, pe_cache, seq_lens, *, q_pe=None, q_out=None, cu_tokens=None,
+                    block_table=None, page_size: int = 64, pos_offset: int = 0, rope_theta: float = 10000.0,
+                    err_flag=None, Lk: Optional[int] = None, stream=None) -> Optional[torch.Tensor]:
+    """Enqueue mla_rope_append: latent rows and rotated rope rows into the cache,
+    in place; returns the rotated queries (None without ``q_pe``).
 
     Without ``cu_tokens``: c_kv (B, Q, 512), k_pe (B, Q, Dr), q_pe (B, Q, H, Dr),
     q_out (B, H, Q, Dr). With ``cu_tokens`` (B+1) int32: c_kv (N, 512), k_pe
     (N, Dr), q_pe and q_out (N, H, Dr). Any strides with a packed last dim
     (slices of wider projection rows); the tokens of c_kv, k_pe and q_pe must
-    step evenly.
+    step evenly. The cache tensors follow make_decode_args; ``seq_lens`` (B) int32
+    are the lengths after the append. A token whose position or page is out of
+    range is not stored and sets DEVICE_ERR_BLOCK_TABLE in ``err_flag``.
     """
-    _same_device(c_kv.get_device(), k_pe, kv_cache, pe_cache, seq_lens, q_pe, q_out, cu_tokens, block_table, err_flag)
-    dtype = c_kv.dtype
-    if not (k_pe.dtype is dtype and kv_cache.dtype is dtype and pe_cache.dtype is dtype and
-            (q_pe is None or q_pe.dtype is dtype) and (q_out is None or q_out.dtype is dtype)):
-        raise MlaError("mla_rope_append: tensors must share one dtype")
-    B = seq_lens.numel()
-    uniform = cu_tokens is None
-    cu = None
-    if not uniform:
-        cu = _int32(cu_tokens, "cu_tokens")
-        if cu_tokens.numel() != B + 1:
-            raise MlaError("cu_tokens must have B + 1 elements")
-    *tokens, Ckv = c_kv.shape
-    *same, Dr = k_pe.shape
-    if same != tokens or len(tokens) != 1 + uniform or (uniform and tokens[0] != B):
-        raise MlaError("mla_rope_append: c_kv and k_pe must be (B, Q, C), or (N, C) with cu_tokens")
-    N, Q = (B * tokens[1], tokens[1]) if uniform else (tokens[0], 0)
-    H = qs = qh = ob = ot = oh = 0
-    qp = op = None
-    if q_pe is not None:
-        *same, H, width = q_pe.shape
-        if same != tokens or width != Dr:
-            raise MlaError("mla_rope_append: q_pe must hold the tokens' heads, Dr wide")
-        shape = (B, H, Q, Dr) if uniform else (N, H, Dr)
-        if q_out is None:
-            q_out = q_pe.new_empty(shape)
-        elif tuple(q_out.shape) != shape or q_out.stride(-1) != 1:
-            raise MlaError(f"mla_rope_append: q_out must be {shape}, last dim packed")
-        qs, qh = _step(q_pe, uniform), q_pe.stride(-2)
-        if uniform:
-            ob, oh, ot, _ = q_out.stride()
-        else:
-            ot, oh, _ = q_out.stride()
-        qp, op = q_pe.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise MlaError("mla_rope_append: q_out without q_pe")
-    kr, pr, kb, pb, Lk, table, max_pages, num_pages = _cache_rows(kv_cache, pe_cache, block_table, page_size, Lk, B,
-                                                                  Ckv, Dr)
-    _int_range(N, pos_offset)
-    a = RopeAppendArgs(B, Q, N, Ckv, Dr, H, _qdtype(c_kv), c_kv.data_ptr(), k_pe.data_ptr(), qp, op,
-                       _step(c_kv, uniform), _step(k_pe, uniform), qs, qh, ob, ot, oh, kv_cache.data_ptr(),
-                       pe_cache.data_ptr(), kr, pr, kb, pb, Lk, _int32(seq_lens, "seq_lens"), table, max_pages,
-                       page_size, num_pages, cu, pos_offset, rope_theta,
-                       None if err_flag is None else _int32(err_flag, "err_flag"))
-    return a, q_out
-
-
-def mla_rope_append(c_kv, k_pe, kv_cache, pe_cache, seq_lens, *, stream=None, **kw) -> Optional[torch.Tensor]:
-    """Enqueue mla_rope_append: latent rows and rotated rope rows into the cache,
-    in place; returns the rotated queries (None without ``q_pe``).
-
-    Arguments as in :func:`make_rope_append_args`; ``seq_lens`` are the lengths
-    after the append. A token whose position or page is out of range is not
-    stored and sets DEVICE_ERR_BLOCK_TABLE in ``err_flag``.
-    """
-    a, q_out = make_rope_append_args(c_kv, k_pe, kv_cache, pe_cache, seq_lens, **kw)
-    L = lib()
-    status = _launch(lambda st: L.mla_rope_append(ctypes.byref(a), st), c_kv.get_device(), stream, q_out)
-    if status:
-        _check(status, "mla_rope_append")
-    return q_out
-
-
-@dataclass
-class PrefixCall:
-    """One mla_prefix_decode call: its arguments, workspace and outputs (build once, launch many times)."""
-
-    args: PrefixArgs
-    num_splits: int
-    workspace: Optional[torch.Tensor]
-    workspace_bytes: int
-    x: torch.Tensor
-    lse: Optional[torch.Tensor]
-    keep: tuple = ()   # tensors the pointers in args refer to
+    return (_step_mod or _step()).rope_append(c_kv, k_pe, kv_cache, pe_cache, seq_lens, q_pe, q_out, cu_tokens,
+                                              block_table, page_size, pos_offset, rope_theta, err_flag, Lk,
+                                              None if stream is None else _stream(stream))
 
 
 def make_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, softmax_scale: float, *,
                        prefix_len: Optional[int] = None, prefix_table=None, seq_lens=None, block_table=None,
                        page_size: int = 64, causal_mask=None, causal: bool = False, sinks=None,
                        num_splits: int = 0, x=None, lse=None, want_lse: bool = True, workspace=None,
-                       err_flag=None, Lk: Optional[int] = None) -> PrefixCall:
-    """Prepare mla_prefix_decode (no GPU work): allocates x, lse and the workspace when not given.
+                       err_flag=None, Lk: Optional[int] = None):
+    """Prepare mla_prefix_decode (no GPU work): a call with ``x``, ``lse``, ``num_splits``,
+    ``workspace`` and ``workspace_bytes``, to launch many times.
 
-    prefix_kv / prefix_pe: (prefix_len, C) rows, or (pages, page_size, C) pools
-    with ``prefix_table`` and ``prefix_len``; None with ``prefix_len`` 0.
-    kv_cache / pe_cache: the sequences' own tokens, laid out as for mla_decode,
-    or None (no own tokens). ``causal_mask`` (uint8 or bool, contiguous) covers
-    prefix_len + Lk positions.
+    Allocates x, lse and the workspace when not given. prefix_kv / prefix_pe:
+    (prefix_len, C) rows, or (pages, page_size, C) pools with ``prefix_table`` and
+    ``prefix_len``; None with ``prefix_len`` 0. kv_cache / pe_cache: the sequences'
+    own tokens, laid out as for mla_decode, or None (no own tokens).
+    ``causal_mask`` (uint8 or bool, contiguous) covers prefix_len + Lk positions.
     """
-    dev = q_lat.get_device()
-    _same_device(dev, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, prefix_table, seq_lens, block_table,
-                 causal_mask, sinks, x, lse, workspace, err_flag)
-    dtype = q_lat.dtype
-    for t in (q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, x):
-        if t is not None and t.dtype is not dtype:
-            raise MlaError("mla_prefix_decode: tensors must share one dtype")
-    if q_lat.dim() != 4:
-        raise MlaError("q_lat must be (B, H, Q, 512)")
-    B, H, Q, Ckv = shape = q_lat.shape
-    Dr, qp = 0, None
-    if q_pe is not None:
-        *same, Dr = q_pe.shape
-        qp = q_pe.data_ptr()
-        if same != [B, H, Q] or not q_pe.is_contiguous():
-            raise MlaError("q_pe must be contiguous (B, H, Q, Dr)")
-    if not q_lat.is_contiguous():
-        raise MlaError("q_lat must be contiguous (B, H, Q, 512)")
-
-    pk = pp = ptab = None
-    pks = pps = p_pages = 0
-    if prefix_kv is None:
-        if prefix_len:
-            raise MlaError("prefix_len without prefix_kv")
-        prefix_len = 0
-    else:
-        paged = prefix_table is not None
-        *rows, width = prefix_kv.shape
-        st = prefix_kv.stride()
-        pk, pks = prefix_kv.data_ptr(), st[-2]
-        if len(rows) != 1 + paged or width < Ckv or st[-1] != 1:
-            raise MlaError("prefix_kv must be (rows, C), or (pages, page_size, C) with prefix_table, last dim packed")
-        if Dr:
-            *same, width = prefix_pe.shape if prefix_pe is not None else (0,)
-            if same != rows or width < Dr or prefix_pe.stride(-1) != 1:
-                raise MlaError("prefix_pe must hold prefix_kv's rows, at least Dr wide, last dim packed")
-            pp, pps = prefix_pe.data_ptr(), prefix_pe.stride(-2)
-        if paged:
-            ptab = _int32(prefix_table, "prefix_table")
-            p_pages = rows[0]
-            if prefix_len is None or rows[1] != page_size or prefix_table.numel() * page_size < prefix_len:
-                raise MlaError("a paged prefix needs prefix_len, pages of page_size rows, and a table that covers it")
-            if p_pages > 1 and (st[0] != page_size * pks or (Dr and prefix_pe.stride(0) != page_size * pps)):
-                raise MlaError("a pool's pages must follow each other")
-        elif prefix_len is None:
-            prefix_len = rows[0]
-        elif prefix_len > rows[0]:
-            raise MlaError("prefix_len is beyond prefix_kv's rows")
-
-    k = p = table = None
-    kr = pr = kb = pb = max_pages = num_pages = 0
-    if kv_cache is not None:
-        kr, pr, kb, pb, Lk, table, max_pages, num_pages = _cache_rows(kv_cache, pe_cache, block_table, page_size, Lk,
-                                                                      B, Ckv, Dr)
-        k, p = kv_cache.data_ptr(), pe_cache.data_ptr() if Dr else None
-    elif Lk:
-        raise MlaError("Lk without kv_cache")
-    Lk = Lk or 0
-    _int_range(prefix_len, Lk, num_splits)
-    lens = None
-    if seq_lens is not None:
-        lens = _int32(seq_lens, "seq_lens")
-        if seq_lens.numel() != B:
-            raise MlaError("seq_lens must have B elements")
-    mask = None
-    if causal_mask is not None:
-        if causal_mask.dtype not in (torch.uint8, torch.bool) or not causal_mask.is_contiguous():
-            raise MlaError("causal_mask must be contiguous uint8 or bool")
-        mask = causal_mask.data_ptr()
-        if causal_mask.numel() < prefix_len + Lk:
-            raise MlaError("causal_mask must cover prefix_len + Lk positions")
-    if sinks is not None and (sinks.dtype is not torch.float32 or not sinks.is_contiguous() or sinks.numel() != H):
-        raise MlaError("sinks must be (H) float32")
-    if x is None:
-        x = torch.empty_like(q_lat)
-    elif not x.is_contiguous() or x.shape != shape:
-        raise MlaError("x must be contiguous (B, H, Q, 512)")
-    if lse is not None:
-        if lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() != B * H * Q:
-            raise MlaError("lse must be contiguous float32 (B, H, Q)")
-    elif want_lse:
-        lse = q_lat.new_empty((B, H, Q), dtype=torch.float32)
-    a = PrefixArgs(B, H, Q, Ckv, Dr, _qdtype(q_lat), q_lat.data_ptr(), qp, pk, pp, pks, pps, prefix_len, ptab, p_pages,
-                   k, p, kr, pr, kb, pb, Lk, lens, table, max_pages, page_size, num_pages, mask, bool(causal),
-                   softmax_scale, _ptr(sinks), num_splits, x.data_ptr(), _ptr(lse),
-                   None if err_flag is None else _int32(err_flag, "err_flag"))
-    L, ref = lib(), ctypes.byref(a)
-    # the split rule reads the current device's SM count
-    if torch.cuda.current_device() == dev:
-        S, need = L.mla_prefix_decode_num_splits(ref), L.mla_prefix_decode_workspace_size(ref)
-    else:
-        with torch.cuda.device(dev):
-            S, need = L.mla_prefix_decode_num_splits(ref), L.mla_prefix_decode_workspace_size(ref)
-    if S < 0:
-        raise MlaError("mla_prefix_decode arguments rejected (MLA_ERR_INVALID_ARG or MLA_ERR_UNSUPPORTED)")
-    if not need:
-        workspace = None
-    elif workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q_lat.device)
-    elif not workspace.is_contiguous() or workspace.nbytes < need:
-        raise MlaError(f"mla_prefix_decode needs a contiguous workspace of {need} bytes")
-    return PrefixCall(a, S, workspace, need, x, lse,
-                      (q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, prefix_table, seq_lens, block_table,
-                       causal_mask, sinks, err_flag))
+    return (_step_mod or _step()).prefix_make(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, softmax_scale,
+                                              prefix_len, prefix_table, seq_lens, block_table, page_size, causal_mask,
+                                              causal, sinks, num_splits, x, lse, want_lse, workspace, err_flag, Lk)
 
 
-def launch_prefix_decode(call: PrefixCall, stream=None):
+def launch_prefix_decode(call, stream=None):
     """Enqueue a prepared call; returns its (x, lse)."""
-    ws, L = call.workspace, lib()
-    status = _launch(lambda st: L.mla_prefix_decode(ctypes.byref(call.args), _ptr(ws), call.workspace_bytes, st),
-                     call.x.get_device(), stream, call.x, call.lse, ws, *call.keep)
-    if status:
-        _check(status, "mla_prefix_decode")
-    return call.x, call.lse
+    return (_step_mod or _step()).prefix_launch(call, None if stream is None else _stream(stream))
 
 
 def mla_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, softmax_scale: float, *,
-                      stream=None, **kw):
+                      prefix_len: Optional[int] = None, prefix_table=None, seq_lens=None, block_table=None,
+                      page_size: int = 64, causal_mask=None, causal: bool = False, sinks=None, num_splits: int = 0,
+                      x=None, lse=None, want_lse: bool = True, workspace=None, err_flag=None,
+                      Lk: Optional[int] = None, stream=None):
     """Decode of a batch that shares a prefix; returns (x, lse), final when the enqueued work completes.
 
     Arguments as in :func:`make_prefix_decode`; ``causal_mask`` may have any dtype
     (0 = hidden). The call merges its split partials itself: there is no combine
     to call after it.
     """
-    mask = kw.get("causal_mask")
-    if mask is not None and (mask.dtype not in (torch.uint8, torch.bool) or not mask.is_contiguous()):
-        _same_device(q_lat.get_device(), mask)
-        with _copies_on(q_lat.get_device(), stream):
-            kw["causal_mask"] = mask.ne(0).contiguous()
-    return launch_prefix_decode(make_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache,
-                                                   softmax_scale, **kw), stream=stream)
+    return (_step_mod or _step()).prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, softmax_scale,
+                                                prefix_len, prefix_table, seq_lens, block_table, page_size,
+                                                causal_mask, causal, sinks, num_splits, x, lse, want_lse, workspace,
+                                                err_flag, Lk, None if stream is None else _stream(stream))
 
 
 def mla_prefix_decode_step(q_nope, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, wkv_b, softmax_scale,
-                           causal_mask=None, **kw):
+                           causal_mask=None, *, stream=None, **kw):
     """mla_decode_step behind a shared prefix -> out (B,H,Q,Vd): absorb, prefix decode, up-project."""
-    Dn, stream, dev = q_nope.shape[-1], kw.get("stream"), q_nope.get_device()
-    _same_device(dev, wkv_b)
-
-    def absorb(st):
-        return mla_absorb_q(q_nope, wkv_b, stream=st)
-
-    q_lat = _launch(absorb, dev, stream)
-    x, _ = mla_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, softmax_scale,
-                             causal_mask=causal_mask, **kw)
-    out = _launch(lambda st: mla_up_proj(x, wkv_b, Dn, stream=st), dev, stream, q_lat, x)
+    _need_cuda(q_nope, wkv_b)
     if stream is not None:
-        _launch(lambda st: None, dev, stream, out)
-    return out
+        # every tensor between the calls is made and used on that stream
+        s = torch.cuda.ExternalStream(_stream(stream), device=q_nope.device)
+        with torch.cuda.stream(s):
+            out = mla_prefix_decode_step(q_nope, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, wkv_b, softmax_scale,
+                                         causal_mask, **kw)
+        out.record_stream(torch.cuda.current_stream(q_nope.device))
+        return out
+    with torch.cuda.device(q_nope.device):
+        q_lat = mla_absorb_q(q_nope, wkv_b)
+        x, _ = mla_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, softmax_scale,
+                                 causal_mask=causal_mask, **kw)
+        return mla_up_proj(x, wkv_b, q_nope.shape[-1])
 
 
 FP4_BLOCK, FP4_ENTRY_BYTES = 512, 288
@@ -871,62 +610,25 @@ def pack_fp4_weight(w: torch.Tensor, scale: Optional[float] = None):
     maximum back to the host. Done once, when weights are loaded, on the current
     stream.
     """
-    dev = w.get_device()
-    _same_device(dev)
+    _need_cuda(w)
     if w.dim() < 2 or w.shape[-1] % FP4_BLOCK or not w.is_floating_point() or w.numel() == 0:
         raise MlaError("pack_fp4_weight: w must be (..., N, K) floating point, K a multiple of 512")
-    wf = w.float()
-    if scale is None:
-        scale = float(wf.abs().max()) / (448.0 * 6.0) or 1.0
-    rows = (wf / scale).reshape(1, -1, FP4_BLOCK).contiguous()
-    n = rows.shape[1]
-    entries = torch.empty((1, n, FP4_ENTRY_BYTES), dtype=torch.uint8, device=w.device)
-    lens = torch.full((1,), n, dtype=torch.int32, device=w.device)
-    _launch(lambda st: mla_cache_append(rows, None, entries, None, lens, stream=st), dev, None)
+    with torch.cuda.device(w.device):
+        wf = w.float()
+        if scale is None:
+            scale = float(wf.abs().max()) / (448.0 * 6.0) or 1.0
+        rows = (wf / scale).reshape(1, -1, FP4_BLOCK).contiguous()
+        n = rows.shape[1]
+        entries = torch.empty((1, n, FP4_ENTRY_BYTES), dtype=torch.uint8, device=w.device)
+        lens = torch.full((1,), n, dtype=torch.int32, device=w.device)
+        mla_cache_append(rows, None, entries, None, lens)
     return entries.reshape(*w.shape[:-1], w.shape[-1] // FP4_BLOCK, FP4_ENTRY_BYTES), scale
-
-
-def _fp4_linear(x, w, dims, strides, scale: float, out, err_flag, stream):
-    """One mla_fp4_linear launch; ``dims`` (B, Q, G, N, K), ``strides`` those of x."""
-    dev = x.get_device()
-    _same_device(dev, w, out, err_flag)
-    if x.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16 or not out.is_contiguous():
-        raise MlaError("mla_fp4_linear takes and gives bf16, out contiguous")
-    if w.dtype is not torch.uint8 or not w.is_contiguous() or w.shape[-1] != FP4_ENTRY_BYTES:
-        raise MlaError("mla_fp4_linear weights are contiguous uint8 entries of 288 bytes")
-    if dims[0] * dims[1] == 0:
-        return out                                # no tokens
-    a = Fp4LinearArgs(*dims, x.data_ptr(), *strides, w.data_ptr(), scale, out.data_ptr(),
-                      None if err_flag is None else _int32(err_flag, "err_flag"))
-    L, ref = lib(), ctypes.byref(a)
-    need = L.mla_fp4_linear_workspace_size(ref)
-    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-    status = _launch(lambda st: L.mla_fp4_linear(ref, _ptr(ws), need, st), dev, stream, x, out, ws)
-    if status:
-        _check(status, "mla_fp4_linear")
-    return out
 
 
 def mla_fp4_linear(x: torch.Tensor, w: torch.Tensor, scale: float = 1.0, *, out: Optional[torch.Tensor] = None,
                    err_flag=None, stream=None) -> torch.Tensor:
     """out[..., n] = scale * sum_k x[..., k] W[n, k]: x (..., K) bf16, w (N, K/512, 288) FP4 entries."""
-    *lead, K = x.shape if x.dim() else (0,)
-    if w.dim() != 3 or K != w.shape[1] * FP4_BLOCK:
-        raise MlaError("mla_fp4_linear: w must be (N, K/512, 288) for x (..., K)")
-    N = w.shape[0]
-    x2 = x
-    if len(lead) != 1 or x.stride(1) != 1 or x.stride(0) % 8 or x.data_ptr() % 16:
-        _same_device(x.get_device())
-        with _copies_on(x.get_device(), stream):
-            x2 = x.contiguous().view(-1, K)
-            if x2.data_ptr() % 16:
-                x2 = x2.clone()
-    step = x2.stride(0)
-    if out is None:
-        out = x.new_empty((*lead, N), dtype=torch.bfloat16)
-    elif list(out.shape) != [*lead, N]:
-        raise MlaError("mla_fp4_linear: out has another shape")
-    return _fp4_linear(x2, w, (x2.shape[0], 1, 1, N, K), (step, 0, 0, FP4_BLOCK), scale, out, err_flag, stream)
+    return (_step_mod or _step()).fp4_linear(x, w, scale, out, err_flag, None if stream is None else _stream(stream))
 
 
 def mla_fp4_group_wo(x: torch.Tensor, wo_a: torch.Tensor, wo_b: Optional[torch.Tensor] = None, *,
@@ -937,24 +639,5 @@ def mla_fp4_group_wo(x: torch.Tensor, wo_a: torch.Tensor, wo_b: Optional[torch.T
     x (B,H,Q,512) bf16; wo_a (G,R,H/G,288) entries of (G, R, (H/G)*512) weights;
     wo_b (D,G*R/512,288). z is rounded to bf16 between the factors, as there.
     """
-    if x.dim() != 4 or x.shape[-1] != FP4_BLOCK or wo_a.dim() != 4:
-        raise MlaError("mla_fp4_group_wo: x must be (B, H, Q, 512) and wo_a (G, R, H/G, 288)")
-    B, H, Q, _ = x.shape
-    G, R, per, _ = wo_a.shape
-    if G * per != H:
-        raise MlaError("mla_fp4_group_wo: wo_a must be (G, R, H/G, 288)")
-    sb, sh, sq, one = x.stride()
-    if one != 1 or sb % 8 or sh % 8 or sq % 8 or x.data_ptr() % 16:
-        _same_device(x.get_device())
-        with _copies_on(x.get_device(), stream):
-            x = x.clone(memory_format=torch.contiguous_format)
-        sb, sh, sq, one = x.stride()
-    z = out if wo_b is None else None
-    if z is None:
-        z = x.new_empty((B, Q, G * R), dtype=torch.bfloat16)
-    elif tuple(z.shape) != (B, Q, G * R):
-        raise MlaError("mla_fp4_group_wo: out has another shape")
-    _fp4_linear(x, wo_a, (B, Q, G, R, per * FP4_BLOCK), (sb, sq, per * sh, sh), scale_a, z, err_flag, stream)
-    if wo_b is None:
-        return z
-    return mla_fp4_linear(z, wo_b, scale_b, out=out, err_flag=err_flag, stream=stream)
+    return (_step_mod or _step()).fp4_group_wo(x, wo_a, wo_b, scale_a, scale_b, out, err_flag,
+                                               None if stream is None else _stream(stream))
