@@ -16,12 +16,13 @@
 // accumulation. The epilogue takes the power of two out again.
 //
 //   x_to_f16      one CTA per (token, group): largest magnitude, then the row.
-//   fp4_linear    one cluster of S CTAs per 256 output rows and 64 tokens, each a
-//                 range of K in entries of 512 channels. TMA brings the rows'
-//                 288-byte entries into a ring; 16 warps decode them, 128 channels
-//                 at a time, straight into the A operand in tensor memory (through
-//                 a shared-memory A tile its writes and reads were the bound); TMA
-//                 brings the tokens' B tile, which both halves of the rows share;
+//   fp4_linear    one cluster of S CTAs per 128 or 256 output rows and 64 tokens,
+//                 each a range of K in entries of 512 channels. TMA brings the
+//                 rows' entries into a ring (codes as two swizzled 128-byte
+//                 blocks, so that the rows' reads hit all banks, and scales); 16
+//                 warps decode them, 128 channels at a time, straight into the A
+//                 operand in tensor memory (through a shared-memory A tile its
+//                 writes and reads were the bound); TMA brings the tokens' B tile;
 //                 one warp issues the MMAs (M = 128, N = tokens). The S partial
 //                 sums meet through distributed shared memory in rank order.
 #include <cuda_fp16.h>
@@ -41,36 +42,46 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kRowsM = 256;                  // output rows per cluster: two halves of an MMA's 128
 constexpr int kTokMax = 64;                  // tokens per cluster
 constexpr int kChunkK = 128;                 // channels per A stage (64 columns a half) and token tile (two swizzled blocks)
 constexpr int kPer = kCkv / kChunkK;         // chunks per entry
-constexpr int kRawBytes = kRowsM * kFp4EntryBytes;
-constexpr int kRaw = 2, kA = 3, kX = 4;      // stages: entries, A chunks, token tiles
-constexpr uint32_t kColA = 128;              // TMEM columns: the halves' sums at 0 and 64, A stages of 128 from 128
+constexpr int kConv = 512;                   // converting threads
 constexpr uint32_t kTmemCols = 512;
-constexpr int kConv = 512;                   // converting threads: two chunks of 256 rows at a time
-constexpr int kThreads = kConv + 64;         // + load warp + MMA warp
 
-enum : int {
-  B_RF = 0,                // [kRaw] entries landed
-  B_RE = B_RF + kRaw,      // [kRaw] entries converted (one arrival per converting warp)
-  B_AF = B_RE + kRaw,      // [kA] A stage written (one arrival per warp of eight)
-  B_AE = B_AF + kA,        // [kA] MMAs over the A stage done
-  B_XF = B_AE + kA,        // [kX] token tile landed
-  B_XE = B_XF + kX,        // [kX] MMAs over the token tile done
-  B_DONE = B_XE + kX,
-  B_COUNT
+// A CTA's rows: kHalves MMAs of 128, which share the token tiles. 256 rows halve
+// the tokens' traffic, 128 spread the weights over twice the CTAs.
+template <int kHalves> struct Shape {
+  static constexpr int kRows = 128 * kHalves;
+  static constexpr int kGroups = 4 / kHalves;            // chunks decoded at a time: four warps per 128 rows
+  static constexpr int kCode = kRows * 128;              // bytes of one of an entry's two code blocks
+  static constexpr int kRawBytes = kRows * kFp4EntryBytes;
+  // stages: entries, A chunks (64 columns a half, behind the halves' sums), token tiles
+  static constexpr int kRaw = 4 / kHalves, kA = 8 / kHalves - 1, kX = 4;
+  static constexpr uint32_t kColA = 64 * kHalves, kColStage = 64 * kHalves;
+  static constexpr size_t smem(int tok_pad) {
+    return (size_t)kRaw * kRawBytes + (size_t)kX * tok_pad * kChunkK * 2 + 1024;
+  }
+  enum : int {
+    B_RF = 0,                // [kRaw] entries landed
+    B_RE = B_RF + kRaw,      // [kRaw] entries converted (one arrival per converting warp)
+    B_AF = B_RE + kRaw,      // [kA] A stage written (one arrival per warp of its group)
+    B_AE = B_AF + kA,        // [kA] MMAs over the A stage done
+    B_XF = B_AE + kA,        // [kX] token tile landed
+    B_XE = B_XF + kX,        // [kX] MMAs over the token tile done
+    B_DONE = B_XE + kX,
+    B_COUNT
+  };
 };
+constexpr int kThreads = kConv + 64;         // + load warp + MMA warp
 
 struct alignas(64) LinearParams {
   CUtensorMap tm_x;                          // scaled activations (K, T, G) float16, box 64 x tokens
-  CUtensorMap tm_w;                          // entries as (words of a row, N, G), box 72 words x 256 rows
+  CUtensorMap tm_code, tm_scale;             // weights as (words of a row, N, G): boxes of 32 and 8 words x rows
   const int* exps;                           // (G, T): token t's row holds x 2^-exps
   __nv_bfloat16* out;
   int T, G, N, K;
   int tok_pad;                               // tokens per cluster, a multiple of 16
-  int tiles;                                 // 128-row tiles per group
+  int tiles;                                 // row tiles per group
   float scale;
   int32_t* err;
 };
@@ -232,9 +243,11 @@ struct Ring {
   }
 };
 
+template <int kHalves>
 __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_constant__ LinearParams P) {
+  using F = Shape<kHalves>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ alignas(8) uint64_t bars[B_COUNT];
+  __shared__ alignas(8) uint64_t bars[F::B_COUNT];
   __shared__ uint32_t tmem_ptr;
   __shared__ int failed;
   const uint32_t raw = smem_u32(smem_raw);
@@ -243,27 +256,31 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return smem_u32(bars + i); };
   const int x_bytes = P.tok_pad * kChunkK * 2;
-  const int off_raw = 0, off_x = kRaw * kRawBytes;
+  constexpr int off_x = F::kRaw * F::kRawBytes;
 
   uint32_t S;
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(S));
   const uint32_t rank = cluster_ctarank();
-  const int tile = blockIdx.x / S;           // (group, 256 rows)
-  const int g = tile / P.tiles, n0 = (tile - g * P.tiles) * kRowsM;
+  const int tile = blockIdx.x / S;           // (group, rows)
+  const int g = tile / P.tiles, n0 = (tile - g * P.tiles) * F::kRows;
   const int t0 = blockIdx.y * kTokMax;
   const int entries = P.K / kCkv;
   const int e_begin = (int)((int64_t)entries * rank / S), ne = (int)((int64_t)entries * (rank + 1) / S) - e_begin;
 
   auto load_entry = [&](int i, int stage) {
-    mbar_arrive_expect_tx(bar(B_RF + stage), kRawBytes);
-    tma_load_3d(sb0 + off_raw + stage * kRawBytes, &P.tm_w, bar(B_RF + stage), (e_begin + i) * (kFp4EntryBytes / 4), n0, g);
+    const uint32_t dst = sb0 + stage * F::kRawBytes, full = bar(F::B_RF + stage);
+    const int word = (e_begin + i) * (kFp4EntryBytes / 4);
+    mbar_arrive_expect_tx(full, F::kRawBytes);
+    tma_load_3d(dst, &P.tm_code, full, word, n0, g);
+    tma_load_3d(dst + F::kCode, &P.tm_code, full, word + 32, n0, g);
+    tma_load_3d(dst + 2 * F::kCode, &P.tm_scale, full, word + 64, n0, g);
   };
   if (threadIdx.x == kConv) {                // the load warp's first lane
-    for (int i = 0; i < B_COUNT; ++i)
-      mbar_init(bar(i), i < B_RE ? 1 : i < B_AF ? kConv / 32 : i < B_AE ? kConv / 64 : 1);
+    for (int i = 0; i < F::B_COUNT; ++i)
+      mbar_init(bar(i), i < F::B_RE ? 1 : i < F::B_AF ? kConv / 32 : i < F::B_AE ? 4 * kHalves : 1);
     failed = 0;
     fence_mbar_init();
-    for (int i = 0; i < kRaw && i < ne; ++i) load_entry(i, i);   // weights do not wait for the first kernel
+    for (int i = 0; i < F::kRaw && i < ne; ++i) load_entry(i, i);   // weights do not wait for the first kernel
   }
   __syncwarp();
   if (warp == kConv / 32 + 1) {
@@ -278,30 +295,32 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
 
   if (warp < kConv / 32) {
     // ------------------------------------------------------------------ converting warps
-    // Warps 0-7 decode rows 0-127, 8-15 the others; of either eight the first four
-    // take an entry's even chunks, the last four its odd ones. A thread
-    // decodes one row's chunk: 64 bytes of codes and eight scales become 64 packed
-    // pairs, the 64 columns of an A stage in the row's TMEM lane.
-    const int half = warp >> 3, r = 128 * half + 32 * (warp & 3) + lane, grp = (warp >> 2) & 1;
-    const uint32_t a_tmem = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColA + 64u * (uint32_t)half;
+    // Four warps decode 128 rows of a chunk; kGroups such groups per half take an
+    // entry's chunks in turn. A thread decodes one row's chunk: 64 bytes of codes
+    // and eight scales become 64 packed pairs, the 64 columns of an A stage in the
+    // row's TMEM lane.
+    const int half = (warp >> 2) / F::kGroups, grp = (warp >> 2) % F::kGroups;
+    const int r = 128 * half + 32 * (warp & 3) + lane;
+    const uint32_t a_tmem = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + F::kColA + 64u * (uint32_t)half;
     const Shifts pw;
-    Ring<kRaw> rr;
-    Ring<kA> ra;                             // of chunk 4e + c, c = grp, grp + 2
-    if (grp) ra.step();
+    Ring<F::kRaw> rr;
+    Ring<F::kA> ra;                          // of chunk 4e + c, c = grp, grp + kGroups, ...
+    for (int i = 0; i < grp; ++i) ra.step();
     for (int e = 0; e < ne && ok; ++e) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(B_RF + rr.stage), rr.par));
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(F::B_RF + rr.stage), rr.par));
       if (!ok) break;
-      const uint8_t* src = smem + off_raw + rr.stage * kRawBytes + r * kFp4EntryBytes;
+      const uint8_t* src = smem + rr.stage * F::kRawBytes;
 #pragma unroll 1
-      for (int c = grp; c < kPer; c += 2) {
+      for (int c = grp; c < kPer; c += F::kGroups) {
         uint4 q[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const uint4*>(src + 64 * c + 16 * i);
-        const uint2 sc = *reinterpret_cast<const uint2*>(src + kCkv / 2 + 8 * c);
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(B_AE + ra.stage), ra.par ^ 1));
+        for (int i = 0; i < 4; ++i)
+          q[i] = *reinterpret_cast<const uint4*>(src + (c >> 1) * F::kCode + r * 128 + 16 * ((4 * (c & 1) + i) ^ (r & 7)));
+        const uint2 sc = *reinterpret_cast<const uint2*>(src + 2 * F::kCode + r * 32 + 8 * c);
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(F::B_AE + ra.stage), ra.par ^ 1));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t col = a_tmem + (uint32_t)(ra.stage * kChunkK);
+        const uint32_t col = a_tmem + (uint32_t)ra.stage * F::kColStage;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t two = (i < 2 ? sc.x : sc.y) >> (16 * (i & 1));
@@ -314,16 +333,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
           decode8(q[i].w, __high2half2(s2), pw, v + 12);
           tmem_st16(col + 16u * i, v);
         }
-        if (c + 2 >= kPer) {                 // the entry is read
+        if (c + F::kGroups >= kPer) {        // the entry is read
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_RE + rr.stage));
+          if (lane == 0) mbar_arrive(bar(F::B_RE + rr.stage));
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_AF + ra.stage));
-        ra.step();
-        ra.step();
+        if (lane == 0) mbar_arrive(bar(F::B_AF + ra.stage));
+        for (int i = 0; i < F::kGroups; ++i) ra.step();
       }
       rr.step();
     }
@@ -331,22 +349,22 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
     // ------------------------------------------------------------------ loads
     pdl_wait();                              // the first kernel's rows
     if (lane == 0) {
-      Ring<kRaw> rr;
-      Ring<kX> rx;
+      Ring<F::kRaw> rr;
+      Ring<F::kX> rx;
       for (int c = 0; c < ne * kPer && ok; ++c) {
-        ok = mbar_wait(bar(B_XE + rx.stage), rx.par ^ 1);
+        ok = mbar_wait(bar(F::B_XE + rx.stage), rx.par ^ 1);
         if (!ok) break;
-        mbar_arrive_expect_tx(bar(B_XF + rx.stage), (uint32_t)x_bytes);
+        mbar_arrive_expect_tx(bar(F::B_XF + rx.stage), (uint32_t)x_bytes);
         const uint32_t xb = sb0 + off_x + rx.stage * x_bytes;
         const int k = e_begin * kCkv + c * kChunkK;
-        tma_load_3d(xb, &P.tm_x, bar(B_XF + rx.stage), k, t0, g);
-        tma_load_3d(xb + P.tok_pad * 128, &P.tm_x, bar(B_XF + rx.stage), k + 64, t0, g);
+        tma_load_3d(xb, &P.tm_x, bar(F::B_XF + rx.stage), k, t0, g);
+        tma_load_3d(xb + P.tok_pad * 128, &P.tm_x, bar(F::B_XF + rx.stage), k + 64, t0, g);
         rx.step();
         // entry c / kPer + kRaw into the stage that entry c / kPer leaves
         if (c % kPer == kPer - 1) {
-          if (c / kPer + kRaw < ne) {
-            ok = mbar_wait(bar(B_RE + rr.stage), rr.par);
-            if (ok) load_entry(c / kPer + kRaw, rr.stage);
+          if (c / kPer + F::kRaw < ne) {
+            ok = mbar_wait(bar(F::B_RE + rr.stage), rr.par);
+            if (ok) load_entry(c / kPer + F::kRaw, rr.stage);
           }
           rr.step();
         }
@@ -357,10 +375,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
     // ------------------------------------------------------------------ MMA issue
     const uint32_t el = elect_one();
     const uint32_t idesc = idesc_f16_f32(128, P.tok_pad);
-    Ring<kX> rx;
-    Ring<kA> ra;
+    Ring<F::kX> rx;
+    Ring<F::kA> ra;
     for (int c = 0; c < ne * kPer; ++c) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(B_XF + rx.stage), rx.par) && mbar_wait(bar(B_AF + ra.stage), ra.par));
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(F::B_XF + rx.stage), rx.par) && mbar_wait(bar(F::B_AF + ra.stage), ra.par));
       if (!ok) break;
       tc_fence_after();
       const uint32_t xb = sb0 + off_x + rx.stage * x_bytes;
@@ -370,16 +388,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            mma_one(el, tmem + 64u * h, tmem + kColA + (uint32_t)(ra.stage * kChunkK + 64 * h + b * 32 + k * 8),
+          for (int h = 0; h < kHalves; ++h)
+            mma_one(el, tmem + 64u * h, tmem + F::kColA + (uint32_t)ra.stage * F::kColStage + (uint32_t)(64 * h + b * 32 + k * 8),
                     desc_advance(bd, 32 * k), idesc, c > 0 || b > 0 || k > 0);
       }
-      commit_one(el, bar(B_AE + ra.stage));
-      commit_one(el, bar(B_XE + rx.stage));
+      commit_one(el, bar(F::B_AE + ra.stage));
+      commit_one(el, bar(F::B_XE + rx.stage));
       ra.step();
       rx.step();
     }
-    if (ok && ne > 0) commit_one(el, bar(B_DONE));
+    if (ok && ne > 0) commit_one(el, bar(F::B_DONE));
   }
   if (!ok) *reinterpret_cast<volatile int*>(&failed) = 1;
   __syncthreads();
@@ -389,10 +407,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
   // this CTA's sums as [token][row] in shared memory (its tiles are used up);
   // rank r sums the cluster's partial results of tokens r, r + S, ... in rank order
   float* part = reinterpret_cast<float*>(smem);
-  if (ne > 0 && !failed && !mbar_wait(bar(B_DONE), 0)) *reinterpret_cast<volatile int*>(&failed) = 1;
+  if (ne > 0 && !failed && !mbar_wait(bar(F::B_DONE), 0)) *reinterpret_cast<volatile int*>(&failed) = 1;
   tc_fence_after();
-  const int half = warp >> 3;
-  for (int c = 16 * ((warp >> 2) & 1); c < P.tok_pad && warp < kConv / 32; c += 32) {
+  const int half = (warp >> 2) / F::kGroups, within = warp % (4 * F::kGroups);   // a warp's half, its number there
+  for (int c = 16 * (within >> 2); c < P.tok_pad && warp < kConv / 32; c += 16 * F::kGroups) {
     uint32_t v[16];
     if (ne > 0) {
       tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(64 * half + c), v);
@@ -402,15 +420,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
       for (int i = 0; i < 16; ++i) v[i] = 0u;
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) part[(c + i) * kRowsM + 128 * half + 32 * (warp & 3) + lane] = __uint_as_float(v[i]);
+    for (int i = 0; i < 16; ++i) part[(c + i) * F::kRows + 128 * half + 32 * (warp & 3) + lane] = __uint_as_float(v[i]);
   }
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && failed && P.err) atomicOr(P.err, MLA_DEVICE_ERR_TIMEOUT);
   cluster_sync();
   const int nt = min(P.tok_pad, P.T - t0);
-  for (int i = (warp & 7) * (int)S + (int)rank; i < nt && warp < kConv / 32; i += kConv / 64 * (int)S) {
-    const uint32_t mine = smem_u32(part + i * kRowsM + 128 * half + 4 * lane);
+  for (int i = within * (int)S + (int)rank; i < nt && warp < kConv / 32; i += 4 * F::kGroups * (int)S) {
+    const uint32_t mine = smem_u32(part + i * F::kRows + 128 * half + 4 * lane);
     float4 v[8];
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k)
@@ -450,13 +468,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-size_t smem_bytes(int tok_pad) { return (size_t)kRaw * kRawBytes + (size_t)kX * tok_pad * kChunkK * 2 + 1024; }
-
 // CTAs per cluster (ranges of K). Clusters of S stay within a GPC, so how many
 // of them run at once is the device's answer, asked once per device and shared
 // memory size: 74, 33, 22, 15 clusters of 2, 4, 6, 8 on a B200. The count taken
 // minimises waves x (entries per CTA + kFixed), kFixed being what a CTA spends
 // besides its entries (launch, first load, exchange), in entries.
+template <int kHalves>
 cudaError_t pick_splits(int64_t clusters, int entries, int tok_pad, int* out) {
   constexpr int kMaxS = 8, kMaxDev = 64, kFixed = 4;
   static std::mutex mu;
@@ -468,9 +485,9 @@ cudaError_t pick_splits(int64_t clusters, int entries, int tok_pad, int* out) {
   std::lock_guard<std::mutex> lock(mu);
   int* act = active[dev][tok_pad / 16 - 1];
   if (!act[0]) {
-    const size_t smem = smem_bytes(tok_pad);
     // the largest size any call needs: the attribute is set once for all of them
-    e = cudaFuncSetAttribute(fp4_linear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(kTokMax));
+    e = cudaFuncSetAttribute(fp4_linear_kernel<kHalves>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)Shape<kHalves>::smem(kTokMax));
     if (e != cudaSuccess) return e;
     for (int S = kMaxS; S >= 1; --S) {
       cudaLaunchConfig_t cfg = {};
@@ -480,11 +497,11 @@ cudaError_t pick_splits(int64_t clusters, int entries, int tok_pad, int* out) {
       attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
       cfg.gridDim = dim3((unsigned)(S * 64));
       cfg.blockDim = dim3(kThreads);
-      cfg.dynamicSmemBytes = smem;
+      cfg.dynamicSmemBytes = Shape<kHalves>::smem(tok_pad);
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       int n = 0;
-      e = cudaOccupancyMaxActiveClusters(&n, fp4_linear_kernel, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&n, fp4_linear_kernel<kHalves>, &cfg);
       if (e != cudaSuccess) return e;
       act[S - 1] = n;                        // [0] last: a filled table
     }
@@ -502,6 +519,45 @@ cudaError_t pick_splits(int64_t clusters, int entries, int tok_pad, int* out) {
   return cudaSuccess;
 }
 
+bool encode(CUtensorMap* m, CUtensorMapDataType type, const void* base, const cuuint64_t* d, const cuuint64_t* s,
+            const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+  const cuuint32_t el[3] = {1, 1, 1};
+  return encode_fn()(m, type, 3, const_cast<void*>(base), d, s, box, el, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The products, with P's activations filled in.
+template <int kHalves>
+cudaError_t launch_products(const mla_fp4_linear_args* a, LinearParams& P, cudaStream_t st) {
+  using F = Shape<kHalves>;
+  const cuuint64_t pitch = (cuuint64_t)(a->K / kCkv) * kFp4EntryBytes;
+  const cuuint64_t d[3] = {pitch / 4, (cuuint64_t)a->N, (cuuint64_t)a->G}, s[2] = {pitch, pitch * a->N};
+  const cuuint32_t code[3] = {32, F::kRows, 1}, scale[3] = {8, F::kRows, 1};
+  if (!encode(&P.tm_code, CU_TENSOR_MAP_DATA_TYPE_UINT32, a->w, d, s, code, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode(&P.tm_scale, CU_TENSOR_MAP_DATA_TYPE_UINT32, a->w, d, s, scale, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorInvalidValue;
+  P.tiles = (a->N + F::kRows - 1) / F::kRows;
+  const int64_t blocks = (P.T + kTokMax - 1) / kTokMax;
+  int S = 0;
+  cudaError_t e = pick_splits<kHalves>((int64_t)a->G * P.tiles * blocks, a->K / kCkv, P.tok_pad, &S);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)S;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)((int64_t)a->G * P.tiles * S), (unsigned)blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = F::smem(P.tok_pad);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, fp4_linear_kernel<kHalves>, P);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 size_t xs_bytes(const mla_fp4_linear_args* a) {
   return ((size_t)a->B * a->Q * a->G * a->K * 2 + 255) & ~(size_t)255;
 }
@@ -512,7 +568,7 @@ size_t fp4_linear_workspace_bytes(const mla_fp4_linear_args* a) {
   return xs_bytes(a) + (size_t)a->B * a->Q * a->G * sizeof(int);
 }
 
-cudaError_t launch_fp4_linear(const mla_fp4_linear_args* a, void* ws, int sms, cudaStream_t st) {
+cudaError_t launch_fp4_linear(const mla_fp4_linear_args* a, void* ws, cudaStream_t st) {
   if (!encode_fn()) return cudaErrorNotSupported;
   LinearParams P;
   memset(static_cast<void*>(&P), 0, sizeof(P));
@@ -528,27 +584,15 @@ cudaError_t launch_fp4_linear(const mla_fp4_linear_args* a, void* ws, int sms, c
   P.scale = a->scale;
   P.err = a->err_flag;
   P.tok_pad = T >= kTokMax ? kTokMax : (T + 15) / 16 * 16;
-  P.tiles = (a->N + kRowsM - 1) / kRowsM;
   {
     const cuuint64_t d[3] = {(cuuint64_t)a->K, (cuuint64_t)T, (cuuint64_t)a->G};
     const cuuint64_t s[2] = {(cuuint64_t)a->K * 2, (cuuint64_t)a->K * 2 * T};
-    const cuuint32_t bx[3] = {64, (cuuint32_t)P.tok_pad, 1}, el[3] = {1, 1, 1};
-    if (encode_fn()(&P.tm_x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, xs, d, s, bx, el, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
-  }
-  {
-    const cuuint64_t pitch = (cuuint64_t)(a->K / kCkv) * kFp4EntryBytes;
-    const cuuint64_t d[3] = {pitch / 4, (cuuint64_t)a->N, (cuuint64_t)a->G}, s[2] = {pitch, pitch * a->N};
-    const cuuint32_t bx[3] = {kFp4EntryBytes / 4, kRowsM, 1}, el[3] = {1, 1, 1};
-    if (encode_fn()(&P.tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(a->w), d, s, bx, el,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    const cuuint32_t bx[3] = {64, (cuuint32_t)P.tok_pad, 1};
+    if (!encode(&P.tm_x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xs, d, s, bx, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)T, (unsigned)a->G);
@@ -556,24 +600,13 @@ cudaError_t launch_fp4_linear(const mla_fp4_linear_args* a, void* ws, int sms, c
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, x_to_f16, *a, xs, exps);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, x_to_f16, *a, xs, exps);
   if (e != cudaSuccess) return e;
-
-  const int64_t clusters = (int64_t)a->G * P.tiles * ((T + kTokMax - 1) / kTokMax);
-  const size_t smem = smem_bytes(P.tok_pad);
-  int S = 0;
-  e = pick_splits(clusters, a->K / kCkv, P.tok_pad, &S);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)((int64_t)a->G * P.tiles * S), (unsigned)((T + kTokMax - 1) / kTokMax));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)S;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, fp4_linear_kernel, P);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  // A CTA brings in 288 bytes of weights a row and entry, and 1024 a token: 256
+  // rows where the tokens' share of 128 would be the larger (64 tokens, 16384 to
+  // 7168: 27 against 29 us), else 128, on twice the CTAs (one token, 8192 to 4096:
+  // 12.5 against ONETOK us).
+  return P.tok_pad > 32 ? launch_products<2>(a, P, st) : launch_products<1>(a, P, st);
 }
 
 }  // namespace mla
