@@ -55,24 +55,30 @@ template <int kHalves> struct Shape {
   static constexpr int kGroups = 4 / kHalves;            // chunks decoded at a time: four warps per 128 rows
   static constexpr int kCode = kRows * 128;              // bytes of one of an entry's two code blocks
   static constexpr int kRawBytes = kRows * kFp4EntryBytes;
-  // stages: entries, A chunks (64 columns a half, behind the halves' sums), token tiles
-  static constexpr int kRaw = 4 / kHalves, kA = 8 / kHalves - 1, kX = 4;
+  // stages: entries, A chunks (64 columns a half, behind the halves' sums)
+  static constexpr int kRaw = 4 / kHalves, kA = 8 / kHalves - 1;
   static constexpr uint32_t kColA = 64 * kHalves, kColStage = 64 * kHalves;
+  // token tiles: as many as the 64 KB beside the entries hold. A tile arrives up to
+  // a microsecond after its request (it queues behind the entries), so few of
+  // them pace the MMAs: 4 tiles of 32 tokens, 0.3 us a chunk.
+  static constexpr int kXMax = 16;
+  static constexpr int x_stages(int tok_pad) { return 65536 / (tok_pad * kChunkK * 2); }
   static constexpr size_t smem(int tok_pad) {
-    return (size_t)kRaw * kRawBytes + (size_t)kX * tok_pad * kChunkK * 2 + 1024;
+    return (size_t)kRaw * kRawBytes + (size_t)x_stages(tok_pad) * tok_pad * kChunkK * 2 + 1024;
   }
   enum : int {
     B_RF = 0,                // [kRaw] entries landed
     B_RE = B_RF + kRaw,      // [kRaw] entries converted (one arrival per converting warp)
     B_AF = B_RE + kRaw,      // [kA] A stage written (one arrival per warp of its group)
     B_AE = B_AF + kA,        // [kA] MMAs over the A stage done
-    B_XF = B_AE + kA,        // [kX] token tile landed
-    B_XE = B_XF + kX,        // [kX] MMAs over the token tile done
-    B_DONE = B_XE + kX,
+    B_XF = B_AE + kA,        // [kXMax] token tile landed
+    B_XE = B_XF + kXMax,     // [kXMax] MMAs over the token tile done
+    B_DONE = B_XE + kXMax,
+    B_GO,                    // the tokens' first tiles landed: the other entries may be requested
     B_COUNT
   };
 };
-constexpr int kThreads = kConv + 64;         // + load warp + MMA warp
+constexpr int kThreads = kConv + 96;         // + entry loads, MMA issue, token loads
 
 struct alignas(64) LinearParams {
   CUtensorMap tm_x;                          // scaled activations (K, T, G) float16, box 64 x tokens
@@ -167,14 +173,21 @@ __device__ __forceinline__ uint32_t elect_one() {
   return e;
 }
 
-// One MMA with A in TMEM, or a commit, by the elected lane (e != 0) of a converged warp.
-__device__ __forceinline__ void mma_one(uint32_t e, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate) {
+// The MMAs of 64 channels (four of K = 16) with A in TMEM, or a commit, by the
+// elected lane (e != 0) of a converged warp. One block of instructions: the issuing
+// warp shares its scheduler with four decoding ones.
+__device__ __forceinline__ void mma_four(uint32_t e, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+      "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(e)
       : "memory");
 }
@@ -231,12 +244,12 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
 }
 
 // A ring position: the stage and the parity of its current pass.
-template <int kStages>
 struct Ring {
-  int stage = 0;
+  int stages, stage = 0;
   uint32_t par = 0;
+  __device__ __forceinline__ explicit Ring(int n) : stages(n) {}
   __device__ __forceinline__ void step() {
-    if (++stage == kStages) {
+    if (++stage == stages) {
       stage = 0;
       par ^= 1;
     }
@@ -260,7 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
 
   uint32_t S;
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(S));
-  const uint32_t rank = cluster_ctarank();
+  S = __shfl_sync(0xffffffffu, S, 0);          // warp-uniform, and so the loops below
+  const uint32_t rank = __shfl_sync(0xffffffffu, cluster_ctarank(), 0);
   const int tile = blockIdx.x / S;           // (group, rows)
   const int g = tile / P.tiles, n0 = (tile - g * P.tiles) * F::kRows;
   const int t0 = blockIdx.y * kTokMax;
@@ -275,12 +289,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
     tma_load_3d(dst + F::kCode, &P.tm_code, full, word + 32, n0, g);
     tma_load_3d(dst + 2 * F::kCode, &P.tm_scale, full, word + 64, n0, g);
   };
-  if (threadIdx.x == kConv) {                // the load warp's first lane
+  // Entries requested at once: what HBM delivers while the first kernel runs. The
+  // others wait for the tokens' first tiles, which come from L2 but queue behind
+  // every entry requested before them (3 us with the whole ring ahead of them).
+  constexpr int kEarly = 1;
+  if (threadIdx.x == kConv) {                // the entry warp's first lane
     for (int i = 0; i < F::B_COUNT; ++i)
       mbar_init(bar(i), i < F::B_RE ? 1 : i < F::B_AF ? kConv / 32 : i < F::B_AE ? 4 * kHalves : 1);
     failed = 0;
     fence_mbar_init();
-    for (int i = 0; i < F::kRaw && i < ne; ++i) load_entry(i, i);   // weights do not wait for the first kernel
+    for (int i = 0; i < kEarly && i < ne; ++i) load_entry(i, i);   // weights do not wait for the first kernel
   }
   __syncwarp();
   if (warp == kConv / 32 + 1) {
@@ -303,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
     const int r = 128 * half + 32 * (warp & 3) + lane;
     const uint32_t a_tmem = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + F::kColA + 64u * (uint32_t)half;
     const Shifts pw;
-    Ring<F::kRaw> rr;
-    Ring<F::kA> ra;                          // of chunk 4e + c, c = grp, grp + kGroups, ...
+    Ring rr(F::kRaw);
+    Ring ra(F::kA);                          // of chunk 4e + c, c = grp, grp + kGroups, ...
     for (int i = 0; i < grp; ++i) ra.step();
     for (int e = 0; e < ne && ok; ++e) {
       ok = __all_sync(0xffffffffu, mbar_wait(bar(F::B_RF + rr.stage), rr.par));
@@ -346,11 +364,24 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
       rr.step();
     }
   } else if (warp == kConv / 32) {
-    // ------------------------------------------------------------------ loads
+    // ------------------------------------------------------------------ entry loads
+    if (lane == 0) {
+      if (ne > kEarly) ok = mbar_wait(bar(F::B_GO), 0);
+      Ring rr(F::kRaw);
+      for (int i = 0; i < kEarly && i < ne; ++i) rr.step();
+      for (int i = kEarly; i < ne && ok; ++i) {
+        ok = i < F::kRaw || mbar_wait(bar(F::B_RE + rr.stage), rr.par ^ 1);
+        if (!ok) break;
+        load_entry(i, rr.stage);
+        rr.step();
+      }
+    }
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+  } else if (warp == kConv / 32 + 2) {
+    // ------------------------------------------------------------------ token loads
     pdl_wait();                              // the first kernel's rows
     if (lane == 0) {
-      Ring<F::kRaw> rr;
-      Ring<F::kX> rx;
+      Ring rx(F::x_stages(P.tok_pad));
       for (int c = 0; c < ne * kPer && ok; ++c) {
         ok = mbar_wait(bar(F::B_XE + rx.stage), rx.par ^ 1);
         if (!ok) break;
@@ -360,13 +391,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
         tma_load_3d(xb, &P.tm_x, bar(F::B_XF + rx.stage), k, t0, g);
         tma_load_3d(xb + P.tok_pad * 128, &P.tm_x, bar(F::B_XF + rx.stage), k + 64, t0, g);
         rx.step();
-        // entry c / kPer + kRaw into the stage that entry c / kPer leaves
-        if (c % kPer == kPer - 1) {
-          if (c / kPer + F::kRaw < ne) {
-            ok = mbar_wait(bar(F::B_RE + rr.stage), rr.par);
-            if (ok) load_entry(c / kPer + F::kRaw, rr.stage);
-          }
-          rr.step();
+        if (c == kPer - 1) {                 // the first entry's
+          ok = mbar_wait(bar(F::B_XF + kPer - 1), 0);
+          mbar_arrive(bar(F::B_GO));
         }
       }
     }
@@ -375,23 +402,20 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
     // ------------------------------------------------------------------ MMA issue
     const uint32_t el = elect_one();
     const uint32_t idesc = idesc_f16_f32(128, P.tok_pad);
-    Ring<F::kX> rx;
-    Ring<F::kA> ra;
+    const uint64_t bd0 = smem_desc(sb0 + off_x, 16, 1024, kSwizzle128B);
+    Ring rx(F::x_stages(P.tok_pad)), ra(F::kA);
     for (int c = 0; c < ne * kPer; ++c) {
       ok = __all_sync(0xffffffffu, mbar_wait(bar(F::B_XF + rx.stage), rx.par) && mbar_wait(bar(F::B_AF + ra.stage), ra.par));
       if (!ok) break;
       tc_fence_after();
-      const uint32_t xb = sb0 + off_x + rx.stage * x_bytes;
+      const uint64_t bd = desc_advance(bd0, rx.stage * x_bytes);
+      const uint32_t at = tmem + F::kColA + (uint32_t)ra.stage * F::kColStage;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const uint64_t bd = smem_desc(xb + b * P.tok_pad * 128, 16, 1024, kSwizzle128B);
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int h = 0; h < kHalves; ++h)
-            mma_one(el, tmem + 64u * h, tmem + F::kColA + (uint32_t)ra.stage * F::kColStage + (uint32_t)(64 * h + b * 32 + k * 8),
-                    desc_advance(bd, 32 * k), idesc, c > 0 || b > 0 || k > 0);
-      }
+        for (int h = 0; h < kHalves; ++h)
+          mma_four(el, tmem + 64u * h, at + (uint32_t)(64 * h + b * 32), desc_advance(bd, b * P.tok_pad * 128), idesc,
+                   c > 0 || b > 0);
       commit_one(el, bar(F::B_AE + ra.stage));
       commit_one(el, bar(F::B_XE + rx.stage));
       ra.step();
