@@ -11,9 +11,10 @@
 // the pipe of the special functions, 16 lanes a clock: 50 us for the 66 MB of
 // the 16384 x 7168 case, where that pipe was 71% busy.) The activations follow: a
 // first kernel scales each token's row by a power of two that brings its
-// largest finite magnitude to [2^14, 2^15) and stores it as float16. bf16 values keep their 8 bits down to 2^-29 of that
-// magnitude, and below it the error is under 2^-40 of it, far below float32's
-// accumulation. The epilogue takes the power of two out again.
+// largest finite magnitude to [2^14, 2^15) and stores it as float16. bf16 values
+// keep their 8 bits down to 2^-29 of that magnitude, and below it the error is
+// under 2^-40 of it, far below float32's accumulation. The epilogue takes the
+// power of two out again.
 //
 //   x_to_f16      one CTA per (token, group): largest magnitude, then the row.
 //   fp4_linear    one cluster of S CTAs per 128 or 256 output rows and 64 tokens,
@@ -25,6 +26,13 @@
 //                 writes and reads were the bound); TMA brings the tokens' B tile;
 //                 one warp issues the MMAs (M = 128, N = tokens). The S partial
 //                 sums meet through distributed shared memory in rank order.
+//
+// Measured per call (two launches): 8192 to 4096, one token, 10.9 us; 8 groups of
+// 4096 to 1024, 32 tokens, 12.5 us; 16384 to 7168, 64 tokens, 30.6 us. With few
+// tokens an MMA takes 24 ns whatever its N (128 of them per CTA), behind 4 us for
+// launch, activations and first entries and before 2 us of exchange. With 64, the
+// tokens' tiles are as many bytes as the weights, and a GPC takes in about 0.87
+// TB/s from L2.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
@@ -59,8 +67,7 @@ template <int kHalves> struct Shape {
   static constexpr int kRaw = 4 / kHalves, kA = 8 / kHalves - 1;
   static constexpr uint32_t kColA = 64 * kHalves, kColStage = 64 * kHalves;
   // token tiles: as many as the 64 KB beside the entries hold. A tile arrives up to
-  // a microsecond after its request (it queues behind the entries), so few of
-  // them pace the MMAs: 4 tiles of 32 tokens, 0.3 us a chunk.
+  // a microsecond or more after its request, as it queues behind the entries.
   static constexpr int kXMax = 16;
   static constexpr int x_stages(int tok_pad) { return 65536 / (tok_pad * kChunkK * 2); }
   static constexpr size_t smem(int tok_pad) {
@@ -74,7 +81,6 @@ template <int kHalves> struct Shape {
     B_XF = B_AE + kA,        // [kXMax] token tile landed
     B_XE = B_XF + kXMax,     // [kXMax] MMAs over the token tile done
     B_DONE = B_XE + kXMax,
-    B_GO,                    // the tokens' first tiles landed: the other entries may be requested
     B_COUNT
   };
 };
@@ -290,9 +296,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
     tma_load_3d(dst + 2 * F::kCode, &P.tm_scale, full, word + 64, n0, g);
   };
   // Entries requested at once: what HBM delivers while the first kernel runs. The
-  // others wait for the tokens' first tiles, which come from L2 but queue behind
-  // every entry requested before them (3 us with the whole ring ahead of them).
-  constexpr int kEarly = 1;
+  // others follow the tokens' first tiles, which come from L2 but queue behind
+  // every entry requested before them (3 us with the whole ring ahead of them;
+  // waiting for the tiles before asking for more left HBM idle, 12.5 -> 13.3 us).
+  constexpr int kEarly = 2 / kHalves;
   if (threadIdx.x == kConv) {                // the entry warp's first lane
     for (int i = 0; i < F::B_COUNT; ++i)
       mbar_init(bar(i), i < F::B_RE ? 1 : i < F::B_AF ? kConv / 32 : i < F::B_AE ? 4 * kHalves : 1);
@@ -365,8 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
     }
   } else if (warp == kConv / 32) {
     // ------------------------------------------------------------------ entry loads
+    pdl_wait();
     if (lane == 0) {
-      if (ne > kEarly) ok = mbar_wait(bar(F::B_GO), 0);
       Ring rr(F::kRaw);
       for (int i = 0; i < kEarly && i < ne; ++i) rr.step();
       for (int i = kEarly; i < ne && ok; ++i) {
@@ -391,10 +398,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
         tma_load_3d(xb, &P.tm_x, bar(F::B_XF + rx.stage), k, t0, g);
         tma_load_3d(xb + P.tok_pad * 128, &P.tm_x, bar(F::B_XF + rx.stage), k + 64, t0, g);
         rx.step();
-        if (c == kPer - 1) {                 // the first entry's
-          ok = mbar_wait(bar(F::B_XF + kPer - 1), 0);
-          mbar_arrive(bar(F::B_GO));
-        }
       }
     }
     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -629,7 +632,7 @@ cudaError_t launch_fp4_linear(const mla_fp4_linear_args* a, void* ws, cudaStream
   // A CTA brings in 288 bytes of weights a row and entry, and 1024 a token: 256
   // rows where the tokens' share of 128 would be the larger (64 tokens, 16384 to
   // 7168: 27 against 29 us), else 128, on twice the CTAs (one token, 8192 to 4096:
-  // 12.5 against ONETOK us).
+  // 12.5 against 10.7 us).
   return P.tok_pad > 32 ? launch_products<2>(a, P, st) : launch_products<1>(a, P, st);
 }
 
