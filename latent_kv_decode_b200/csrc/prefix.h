@@ -57,21 +57,22 @@ __device__ __forceinline__ int prefix_len_of(const PrefixParams& p, int b) {
 
 // The tiles of TILE tokens that a block of rows walks: the prefix's, then each
 // of its sequences' own. `b` is -1 in the prefix; tokens [t, end) of that
-// source are in the tile.
+// source are in the tile. `lens` holds the own lengths of the block's sequences
+// b0 .. b1, read once into shared memory.
 template <int TILE>
 struct TileWalk {
   int b, last, t, end;
 
   __device__ __forceinline__ static int tiles_of(int len) { return (len + TILE - 1) / TILE; }
 
-  // all tiles of the block whose sequences are b0 .. b1
-  __device__ __forceinline__ static int count(const PrefixParams& p, int b0, int b1) {
+  // all tiles of the block
+  __device__ __forceinline__ static int count(const PrefixParams& p, const int* lens, int b0, int b1) {
     int n = tiles_of(p.Lp);
-    for (int b = b0; b <= b1; ++b) n += tiles_of(prefix_len_of(p, b));
+    for (int b = b0; b <= b1; ++b) n += tiles_of(lens[b - b0]);
     return n;
   }
   // position at tile `skip` of the block
-  __device__ __forceinline__ void seek(const PrefixParams& p, int b0, int b1, int skip) {
+  __device__ __forceinline__ void seek(const PrefixParams& p, const int* lens, int b0, int b1, int skip) {
     b = -1;
     last = b1;
     end = p.Lp;
@@ -82,17 +83,17 @@ struct TileWalk {
         t = end = 0;
         return;
       }
-      end = prefix_len_of(p, b);
+      end = lens[b - b0];
     }
     t = skip * TILE;
   }
-  __device__ __forceinline__ void next(const PrefixParams& p, int b0) {
+  __device__ __forceinline__ void next(const int* lens, int b0) {
     t += TILE;
     while (t >= end) {
       b = b < 0 ? b0 : b + 1;
       if (b > last) return;
       t = 0;
-      end = prefix_len_of(p, b);
+      end = lens[b - b0];
     }
   }
 };

@@ -115,7 +115,10 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
   const int r0 = blockIdx.x * kRows, z = blockIdx.y;
   const int nr = min(kRows, p.N - r0);
   const int b0 = r0 / p.HQ, b1 = (r0 + nr - 1) / p.HQ;
-  const int tiles = TileWalk<kToks>::count(p, b0, b1);
+  __shared__ int lens[kRows / 8 + 1];            // H*Q >= 8: the sequences a block can hold rows of
+  if (tid <= b1 - b0) lens[tid] = prefix_len_of(p, b0 + tid);
+  __syncthreads();
+  const int tiles = TileWalk<kToks>::count(p, lens, b0, b1);
   const int per = (tiles + p.num_splits - 1) / p.num_splits;
   const int j0 = min(tiles, z * per), j1 = min(tiles, j0 + per);
 
@@ -152,13 +155,13 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
                         [&](int r) { return row_pe[s][r]; });
   };
   TileWalk<kToks> w, wn;                         // this tile and the next
-  w.seek(p, b0, b1, j0);
+  w.seek(p, lens, b0, b1, j0);
   wn = w;
   if (j0 < j1) {
     locate(w, 0);
     __syncthreads();
     fetch(0);
-    wn.next(p, b0);
+    wn.next(lens, b0);
   }
   copy_commit();
 
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
     const int r = r0 + 4 * warp + 2 * i + sub;
     row_b[i] = r < p.N ? r / p.HQ : -2;
     row_lim[i] = 0x7fffffff;
-    if (r < p.N && p.causal) row_lim[i] = prefix_len_of(p, row_b[i]) - p.Q + r % p.Q;
+    if (r < p.N && p.causal) row_lim[i] = lens[row_b[i] - b0] - p.Q + r % p.Q;
   }
   // O: rows 8 rg + i, columns 4 cg + k and 256 + 4 cg + k
   const int rg = tid >> 6, cg = tid & 63;
@@ -291,7 +294,7 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
       }
     }
     w = wn;
-    if (more) wn.next(p, b0);
+    if (more) wn.next(lens, b0);
   }
 
   // the rows' denominators to the accumulator's threads

@@ -34,7 +34,15 @@
 // the rows no query may see, and if S shows a non-finite key, the softmax warps
 // zero the non-finite values (the rows that see that key are NaN by their S).
 //
-// Warps (384 threads): 0 own-token producer (+ Q), 1 QK issuer (CTA 0) and TMEM
+// A tile's 17 + 16 MMA steps of K = 64 take about 2870 SM cycles in the tensor
+// pipe; a tile takes 3010 (1.53 us), 0.95 of that. The GPCs with 18 or 20 SMs
+// stay a little behind the one with 12: every SM draws 104 KB a tile from L2, and
+// a GPC about 0.87 TB/s. Measured (whole call, merge included): 128 sequences of
+// 16 heads x 2 queries behind 16384 tokens 169 us, 64 of 128 heads behind 4096
+// tokens 83 us, 4 of 128 heads behind 131072 tokens 154 us: 0.87, 0.93 and 0.95
+// PFLOP/s.
+//
+// Warps (384 threads): 0 own-token producer, 1 QK issuer (CTA 0) and TMEM
 // owner, 2 peer-token producer and cleaner, 3 PV issuer (CTA 0), 4-11 softmax +
 // epilogue (TMEM lane = 32 (warp % 4) + lane; the two sets of four split a lane's
 // 64 scores). Every wait is bounded; a timeout sets MLA_DEVICE_ERR_TIMEOUT
@@ -82,13 +90,15 @@ enum : int {
   B_ZD = 32,              // [2] this CTA's rows of a guarded tile are clean (phase: guarded tiles so far)
   B_COUNT = 34
 };
-// Control block: barriers, TMEM address, abort flag, the peer's flags. In the
+// Control block: barriers, TMEM address, abort flag, the peer's flags, lengths. In the
 // alignment gap below the operand region when it fits there, else after the
 // exchange block (row statistics, rescale factors, output scales).
 constexpr int kOffTmemPtr = 8 * B_COUNT;
 constexpr int kOffAbort = kOffTmemPtr + 4;
 constexpr int kOffFlags = (kOffAbort + 4 + 15) & ~15;     // int [2 tiles][16 warps of the peer]
-constexpr int kCtrlBytes = kOffFlags + 2 * kSoftWarps * 4;
+constexpr int kMaxSeqs = kRowsT / 8 + 1;                  // H*Q >= 8: the sequences a block can hold rows of
+constexpr int kOffLens = kOffFlags + 2 * kSoftWarps * 4;  // int [kMaxSeqs]: their own lengths
+constexpr int kCtrlBytes = (kOffLens + kMaxSeqs * 4 + 15) & ~15;
 constexpr int kOffXmax = kBigBytes;                       // float [sets][128 lanes]
 constexpr int kOffAlpha = kOffXmax + 512 * kSets;                // float [128]
 constexpr int kOffScl = kOffAlpha + 512;                  // float [128]
@@ -211,7 +221,8 @@ __device__ __forceinline__ Block64 block64(const PrefixParams& p, const TileWalk
 // entry? Shared by n threads. Looked up once, the common answer spares every
 // softmax thread two table lookups a tile (182 -> 168 us for 128 sequences, 16
 // heads, a 16384-token paged prefix).
-__device__ __forceinline__ bool bad_pages(const PrefixParams& p, int b0, int b1, int j0, int nt, int tid, int n) {
+__device__ __forceinline__ bool bad_pages(const PrefixParams& p, const int* lens, int b0, int b1, int j0, int nt, int tid,
+                                          int n) {
   bool bad = false;
   const int64_t ps = p.page_size;
   if (p.ptable) {
@@ -221,7 +232,7 @@ __device__ __forceinline__ bool bad_pages(const PrefixParams& p, int b0, int b1,
   if (p.table)
     for (int b = b0; b <= b1; ++b) {
       const int32_t* t = p.table + (int64_t)b * p.max_pages;
-      const int len = prefix_len_of(p, b);
+      const int len = lens[b - b0];
       for (int64_t i = tid; i * ps < len; i += n) bad = bad || t[i] < 0 || t[i] >= p.num_pages;
     }
   return bad;
@@ -266,13 +277,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
   pdl_wait();
   const int r0 = rb * kRowsT;
   const int b0 = r0 / p.HQ, b1 = (min(p.N, r0 + kRowsT) - 1) / p.HQ;
-  const int tiles = TileWalk<kTileT>::count(p, b0, b1);
+  const bool rope = p.Dr > 0;
+  int* lens = reinterpret_cast<int*>(ctrl_p + kOffLens);
+  if (threadIdx.x == 0) {
+    // the query rows do not wait for the lengths (with the lengths kept in shared
+    // memory: 177 -> 169 us and 88 -> 83 us, the first two sizes above)
+    const int qrow = r0 + (int)rank * 64;
+    const uint32_t qbar = map_to_rank(bar(B_QFULL), 0);
+    if (rank == 0) mbar_arrive_expect_tx(bar(B_QFULL), 2 * (rope ? 9 : 8) * kChunk);
+    if (rope) tma_load_2d_2sm(sb0 + kOffQ + 8 * kChunk, &P.tm_qpe, qbar, 0, qrow);
+    for (int c = 0; c < 8; ++c) tma_load_2d_2sm(sb0 + kOffQ + c * kChunk, &P.tm_q, qbar, 64 * c, qrow);
+  } else if (threadIdx.x >= 32 && threadIdx.x - 32 <= b1 - b0) {
+    lens[threadIdx.x - 32] = prefix_len_of(p, b0 + (int)threadIdx.x - 32);
+  }
+  __syncthreads();
+  const int tiles = TileWalk<kTileT>::count(p, lens, b0, b1);
   const int per = (tiles + p.num_splits - 1) / p.num_splits;
   const int j_begin = min(tiles, z * per);
   const int ntiles = __shfl_sync(0xffffffffu, min(tiles, j_begin + per) - j_begin, 0);
   TileWalk<kTileT> w;
-  w.seek(p, b0, b1, j_begin);
-  const bool rope = p.Dr > 0;
+  w.seek(p, lens, b0, b1, j_begin);
 
   auto fail = [&]() {
     *abort_flag = 1;
@@ -288,11 +312,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
   if (warp == 0) {
     // ------------------------------------------------------------------ own-token producer
     if (lane == 0 && ntiles > 0) {
-      const int qrow = r0 + (int)rank * 64;
-      const uint32_t qbar = map_to_rank(bar(B_QFULL), 0);
-      if (rank == 0) mbar_arrive_expect_tx(bar(B_QFULL), 2 * (rope ? 9 : 8) * kChunk);
-      if (rope) tma_load_2d_2sm(sb0 + kOffQ + 8 * kChunk, &P.tm_qpe, qbar, 0, qrow);
-      for (int c = 0; c < 8; ++c) tma_load_2d_2sm(sb0 + kOffQ + c * kChunk, &P.tm_q, qbar, 64 * c, qrow);
       bool ok = true;
       for (int j = 0; j < ntiles && ok; ++j) {
         const int s = j & 1;
@@ -313,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
                           ((i & 1) << 2) | (i & 2), k.zc);
         }
         if (*abort_flag) ok = false;
-        w.next(p, b0);
+        w.next(lens, b0);
       }
       if (!ok) {
         fail();
@@ -331,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
     // its own box itself, cleans it, and vouches for it through P's barrier.
     bool ok = true;
     int ng = 0;
-    const bool look = __any_sync(0xffffffffu, bad_pages(p, b0, b1, j_begin, ntiles, lane, 32));
+    const bool look = __any_sync(0xffffffffu, bad_pages(p, lens, b0, b1, j_begin, ntiles, lane, 32));
     for (int j = 0; j < ntiles && ok; ++j) {
       const int s = j & 1;
       const Block64 peer = block64(p, w, 1 - (int)rank);
@@ -377,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
       }
       if (*abort_flag) ok = false;
       ok = __all_sync(0xffffffffu, ok);
-      w.next(p, b0);
+      w.next(lens, b0);
     }
     if (!ok && lane == 0) {
       fail();
@@ -501,9 +520,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
     const float sl2 = P.scale_log2;
     const uint8_t* mask = p.mask;
     // the last token a causal row sees, as a position (own token 0 is at Lp)
-    const int last_pos = !live ? -1 : p.causal ? p.Lp + prefix_len_of(p, my_b) - p.Q + r % p.Q : 0x3fffffff;
+    const int last_pos = !live ? -1 : p.causal ? p.Lp + lens[my_b - b0] - p.Q + r % p.Q : 0x3fffffff;
 
-    const bool look = bar_or(1, kSoft, bad_pages(p, b0, b1, j_begin, ntiles, xi, kSoft));
+    const bool look = bar_or(1, kSoft, bad_pages(p, lens, b0, b1, j_begin, ntiles, xi, kSoft));
 
     for (int j = 0; j < ntiles; ++j) {
       const int sb = j & 1;
@@ -567,8 +586,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
 #pragma unroll
       for (int c = 0; c < kTok; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], e[c]);
       const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-      // the row's reference has to move: its first visible score, or one far above it
-      const bool need = m_run == -INFINITY ? mx > -INFINITY : mx > kMove;
+      // the row's first visible score sets its reference (its O is 0 so far); one
+      // far above the reference moves it, and O^T of both CTAs with it
+      const bool first = m_run == -INFINITY && mx > -INFINITY;
+      const bool need = m_run != -INFINITY && mx > kMove;
       const bool warp_need = __any_sync(0xffffffffu, need);
       if (lane == 0) st_async_b32(peer_flag + 4u * kSoftWarps * (uint32_t)sb, warp_need ? 1u : 0u, map_to_rank(bar(B_AX + sb), peer));
 
@@ -600,26 +621,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
       bool peer_need = false;
 #pragma unroll
       for (int k = 0; k < kSoftWarps; ++k) peer_need = peer_need || flags[kSoftWarps * sb + k] != 0;
-      if (bar_or(1, kSoft, need || odd || peer_need || ab)) {
-        // the rare tile: a reference moves in one of the CTAs (the first tile a
-        // row sees), or a non-finite key has to be silenced
+      if (bar_or(1, kSoft, first || need || odd || peer_need || ab)) {
+        // the rare tile: a reference is set, or moves in one of the CTAs, or a
+        // non-finite key has to be silenced
         if (bar_or(1, kSoft, ab)) {
           ab = true;
           break;
         }
+        const bool set = bar_or(1, kSoft, first || need || peer_need);
         const bool move = bar_or(1, kSoft, need || peer_need);   // both CTAs agree
         const bool dirty = bar_or(1, kSoft, odd);
-        if (move) {
-          if (leader) mbar_arrive_expect_tx(bar(B_AL), 64 * 4);
+        float alpha = 1.f;
+        if (set) {
+          if (leader && move) mbar_arrive_expect_tx(bar(B_AL), 64 * 4);
           const float m_all = across(mx + m_sub, [](float a, float b) { return fmaxf(a, b); });
           const bool mv = m_run == -INFINITY ? m_all > -INFINITY : m_all > m_run + kMove;
-          const float alpha = mv && m_run != -INFINITY ? exp2f(m_run - m_all) : 1.f;
+          alpha = mv && m_run != -INFINITY ? exp2f(m_run - m_all) : 1.f;
           if (mv) m_run = m_all;
           l_part *= alpha;
           load_scores();
           scale_scores(m_run == -INFINITY ? 0.f : m_run);
           weights();
           store_weights();
+        }
+        if (move) {
           // O^T's columns are rows of both CTAs: both rescale their dims of all 128
           if (owner) {
             alpha_s[col] = alpha;
@@ -668,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
         ++ng;
       }
       if (leader) mbar_arrive_remote_cta(map_to_rank(bar(B_PFULL + sb), 0));
-      w.next(p, b0);
+      w.next(lens, b0);
     }
 
     // ---------------------------------------------------------------- epilogue
@@ -757,6 +782,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
   }
 
   // ------------------------------------------------------------------ teardown
+  // an empty range still has its query rows in flight (both CTAs' on CTA 0's barrier)
+  if (ntiles == 0 && rank == 0 && threadIdx.x == 0 && !mbar_wait_cluster(bar(B_QFULL), 0)) fail();
   tc_fence_before();
   __syncthreads();
   cluster_sync();
