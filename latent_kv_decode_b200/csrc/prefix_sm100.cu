@@ -376,11 +376,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_
           for (int i0 = 0; i0 < 64; i0 += 32) {
             const int i = 64 * h + i0 + lane;
             const bool bad = !page_ok || w.t + i >= w.end || (p.mask && p.mask[pos0 + i] == 0);
-            for (uint32_t m = __ballot_sync(0xffffffffu, bad); m; m &= m - 1) {
-              const int tok = i0 + __ffs(m) - 1;
-              *reinterpret_cast<uint4*>(smem + kOffL + (s * 8 + 4 * h + (lane >> 3)) * kChunk + tok * 128 +
-                                        16 * (lane & 7)) = make_uint4(0u, 0u, 0u, 0u);
-            }
+            const uint32_t m = __ballot_sync(0xffffffffu, bad);
+            uint8_t* rows = smem + kOffL + (s * 8 + 4 * h + (lane >> 3)) * kChunk + i0 * 128 + 16 * (lane & 7);
+            if (m == 0) continue;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if ((m >> k) & 1u) *reinterpret_cast<uint4*>(rows + 128 * k) = make_uint4(0u, 0u, 0u, 0u);
           }
         };
         if (rank == 1) ok = mbar_wait_cluster(bar(B_SFULL + s), (j >> 1) & 1);
