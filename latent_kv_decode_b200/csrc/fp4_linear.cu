@@ -1,4 +1,5 @@
-// Products of few tokens with weights held as FP4 entries (mla_fp4_linear).
+// Products of few tokens with weights held as FP4 entries (mla_fp4_linear); the
+// fewest tokens go to fp4_few.cu's kernel.
 //
 // The weights are the bytes: 0.5625 per element, read once per 64 tokens. What
 // it takes to stream them is to turn 4-bit codes into tensor-core operands as
@@ -27,9 +28,8 @@
 //                 one warp issues the MMAs (M = 128, N = tokens). The S partial
 //                 sums meet through distributed shared memory in rank order.
 //
-// Measured per call (two launches): 8192 to 4096, one token, 10.9 us; 8 groups of
-// 4096 to 1024, 32 tokens, 12.5 us; 16384 to 7168, 64 tokens, 30.6 us. With few
-// tokens an MMA takes 24 ns whatever its N (128 of them per CTA), behind 4 us for
+// Measured per call (two launches): 8 groups of 4096 to 1024, 32 tokens, 12.5 us;
+// 16384 to 7168, 64 tokens, 30.7 us. With few tokens an MMA takes 24 ns whatever its N (128 of them per CTA), behind 4 us for
 // launch, activations and first entries and before 2 us of exchange. With 64, the
 // tokens' tiles are as many bytes as the weights, and a GPC takes in about 0.87
 // TB/s from L2.
@@ -592,10 +592,12 @@ size_t xs_bytes(const mla_fp4_linear_args* a) {
 }  // namespace
 
 size_t fp4_linear_workspace_bytes(const mla_fp4_linear_args* a) {
+  if (fp4_few_tokens(a)) return 0;
   return xs_bytes(a) + (size_t)a->B * a->Q * a->G * sizeof(int);
 }
 
-cudaError_t launch_fp4_linear(const mla_fp4_linear_args* a, void* ws, cudaStream_t st) {
+cudaError_t launch_fp4_linear(const mla_fp4_linear_args* a, void* ws, int sms, cudaStream_t st) {
+  if (fp4_few_tokens(a)) return launch_fp4_few(a, sms, st);
   if (!encode_fn()) return cudaErrorNotSupported;
   LinearParams P;
   memset(static_cast<void*>(&P), 0, sizeof(P));

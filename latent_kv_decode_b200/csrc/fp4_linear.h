@@ -9,6 +9,8 @@
 namespace mla {
 
 size_t fp4_linear_workspace_bytes(const mla_fp4_linear_args* a);
-cudaError_t launch_fp4_linear(const mla_fp4_linear_args* a, void* ws, cudaStream_t st);
+bool fp4_few_tokens(const mla_fp4_linear_args* a);          // the calls launch_fp4_few takes
+cudaError_t launch_fp4_few(const mla_fp4_linear_args* a, int sms, cudaStream_t st);
+cudaError_t launch_fp4_linear(const mla_fp4_linear_args* a, void* ws, int sms, cudaStream_t st);
 
 }  // namespace mla

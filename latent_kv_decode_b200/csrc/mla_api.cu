@@ -611,5 +611,5 @@ extern "C" mla_status_t mla_fp4_linear(const mla_fp4_linear_args* a, void* works
   if (s != MLA_OK) return s;
   const size_t need = mla::fp4_linear_workspace_bytes(a);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return MLA_ERR_WORKSPACE;
-  return cuda_status(mla::launch_fp4_linear(a, workspace, (cudaStream_t)stream));
+  return cuda_status(mla::launch_fp4_linear(a, workspace, sm_count(), (cudaStream_t)stream));
 }

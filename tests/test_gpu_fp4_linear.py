@@ -56,6 +56,28 @@ def test_tokens_rows_and_widths(T, N, K):
     _check(y, x.double(), _values(w), 0.013)
 
 
+@pytest.mark.parametrize("T", [1, 3, 8, 9, 16])
+@pytest.mark.parametrize("N,K", [(20, 8704), (2500, 4608), (5001, 2560)])
+def test_few_tokens_with_many_entries_and_rows(T, N, K):
+    """More entries than a CTA has warps; one, two and more CTAs per SM."""
+    from latent_kv_decode_b200 import ops
+    w = _entries((N, K // 512), seed=N)
+    x = torch.randn(T, K, generator=torch.Generator().manual_seed(T + 20)).bfloat16()
+    y = ops.mla_fp4_linear(x.cuda(), w.cuda(), 0.01)
+    _check(y, x.double(), _values(w), 0.01)
+    # a token's result does not depend on the tokens beside it
+    assert torch.equal(ops.mla_fp4_linear(x[-1:].cuda(), w.cuda(), 0.01)[0], y[-1])
+
+
+@pytest.mark.parametrize("p", [-130, -126, -100, -30, 30, 100, 115])
+def test_one_token_over_bf16s_whole_range(p):
+    from latent_kv_decode_b200 import ops
+    w = _entries((33, 2), seed=3)
+    x = (torch.randn(1, 1024, generator=torch.Generator().manual_seed(4)).double() * 2.0 ** p).bfloat16()
+    y = ops.mla_fp4_linear(x.cuda(), w.cuda(), 2.0 ** -16 if p > 0 else 1.0)
+    _check(y, x.double(), _values(w), 2.0 ** -16 if p > 0 else 1.0)
+
+
 @pytest.mark.parametrize("B,H,Q,G,R", [(1, 2, 1, 2, 5), (3, 16, 2, 4, 128), (5, 8, 4, 8, 257), (32, 64, 1, 8, 1024)])
 def test_groups_and_strided_heads(B, H, Q, G, R):
     from latent_kv_decode_b200 import ops
