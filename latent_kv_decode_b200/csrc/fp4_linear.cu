@@ -29,10 +29,10 @@
 //                 sums meet through distributed shared memory in rank order.
 //
 // Measured per call (two launches): 8 groups of 4096 to 1024, 32 tokens, 12.5 us;
-// 16384 to 7168, 64 tokens, 30.7 us. With few tokens an MMA takes 24 ns whatever its N (128 of them per CTA), behind 4 us for
-// launch, activations and first entries and before 2 us of exchange. With 64, the
-// tokens' tiles are as many bytes as the weights, and a GPC takes in about 0.87
-// TB/s from L2.
+// 16384 to 7168, 64 tokens, 30.7 us. With few tokens an MMA takes 24 ns whatever
+// its N (128 of them per CTA), behind 4 us for launch, activations and first entries
+// and before 2 us of exchange. With 64, the tokens' tiles are as many bytes as the
+// weights, and a GPC takes in about 0.87 TB/s from L2.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>

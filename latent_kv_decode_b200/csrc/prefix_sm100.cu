@@ -35,12 +35,13 @@
 // zero the non-finite values (the rows that see that key are NaN by their S).
 //
 // A tile's 17 + 16 MMA steps of K = 64 take about 2870 SM cycles in the tensor
-// pipe; a tile takes 3010 (1.53 us), 0.95 of that. The GPCs with 18 or 20 SMs
-// stay a little behind the one with 12: every SM draws 104 KB a tile from L2, and
-// a GPC about 0.87 TB/s. Measured (whole call, merge included): 128 sequences of
-// 16 heads x 2 queries behind 16384 tokens 169 us, 64 of 128 heads behind 4096
-// tokens 83 us, 4 of 128 heads behind 131072 tokens 154 us: 0.87, 0.93 and 0.95
-// PFLOP/s.
+// pipe (1.46 us); a tile takes 1.53 us in a small GPC and 1.7 with all 74 clusters
+// busy, 1.47 PFLOP/s, where the power limit (1.42 for a long library product)
+// comes into sight. Not loading the other CTA's tokens at all (32 of 104 KB a tile)
+// gains 2%. Measured (whole call, merge included): 128 sequences of 16 heads x 2
+// queries behind 16384 tokens 164 us, 64 of 128 heads behind 4096 tokens 81 us, 4 of
+// 128 heads behind 131072 tokens 153 us: 0.90, 0.96 and 0.96 PFLOP/s, with 64, 64 and
+// 72 clusters.
 //
 // Warps (384 threads): 0 own-token producer, 1 QK issuer (CTA 0) and TMEM
 // owner, 2 peer-token producer and cleaner, 3 PV issuer (CTA 0), 4-11 softmax +
