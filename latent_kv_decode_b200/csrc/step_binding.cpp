@@ -2,7 +2,8 @@
 // and mla_fp4_linear in C++. At a decode step's sizes these calls take the GPU a
 // few microseconds, less than Python needs to read the sizes and strides of a
 // dozen tensors (measured on B200's host: 20, 22 and 13 us a call through ctypes
-// structs, 6, 9 and 5 here, 8 where the product takes two launches). It checks, allocates, fills the argument structs of
+// structs, 6, 9 and 5 here, 8 where the product takes two launches). It checks,
+// allocates, fills the argument structs of
 // include/mla.h and calls libmla.so on the caller's stream; ops.py holds the
 // signatures and their documentation.
 #include <ATen/core/Tensor.h>

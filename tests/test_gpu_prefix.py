@@ -293,6 +293,29 @@ def test_scores_that_climb_far_above_the_first_tile():
     assert ((lse.cpu().double() - lo).abs() <= rel).all()
 
 
+@pytest.mark.parametrize("Lp", [0, 70])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_references_that_start_and_move_in_either_half_of_a_block(Lp, splits):
+    # eight sequences share a block of 128 rows, four in each CTA of its pair; their
+    # rows see a first token in different tiles, and some grow far above it
+    lens = [10, 300, 129, 0, 260, 1, 300, 200]
+    d = _case(8, 16, 1, 64, Lp, lens, seed=21)
+    for b, f in ((1, 60.0), (2, 40.0), (6, 70.0), (7, 8.0)):
+        own = d["kv"][b]
+        own[128:lens[b]] = (own[128:lens[b]].double() * f).to(own.dtype)
+        d["rows"][b][Lp:, :C] = own[:lens[b]].cpu().double()
+    x, lse, err = _run(d, num_splits=splits)
+    assert err == 0
+    xo, lo, bound = _oracle(d)
+    fin = torch.isfinite(lo)
+    # as above: 576 * 2^-24 of sum |q k| scale <= 4e3 moves every weight
+    rel = 576 * 2.0 ** -24 * 4e3
+    big = max(r.abs().max().item() for r in d["rows"] if len(r))
+    assert ((x.cpu().double() - xo).abs()[fin] <= (bound + rel * big)[fin]).all()
+    assert ((lse.cpu().double() - lo).abs()[fin] <= rel).all()
+    assert (x.cpu()[~fin] == 0).all() and (lse.cpu()[~fin] == -math.inf).all()
+
+
 def test_strided_rows_and_separate_storage():
     d = _case(4, 16, 1, 64, 300, [3, 70, 128, 1], pad=64, seed=15)            # 640-wide rows
     _check(d)
