@@ -258,26 +258,30 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(acc[i][k]) : "l"(al2));
     }
+    const int nt = min(kToks, w.end - w.t);      // tokens past it have no weight
     if (!any_odd) {
-#pragma unroll 4
-      for (int tt = 0; tt < kToks; ++tt) {
-        const f32x4 v0 = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 4 * cg);
-        const f32x4 v1 = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 256 + 4 * cg);
-        const float4 pa = *reinterpret_cast<const float4*>(ps + tt * kRows + 8 * rg);
-        const float4 pb = *reinterpret_cast<const float4*>(ps + tt * kRows + 8 * rg + 4);
-        const float pr[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+#pragma unroll 1
+      for (int t4 = 0; t4 < nt; t4 += 4) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const f32x2 p2 = pack2(pr[i], pr[i]);
-          fma2(acc[i][0], p2, v0.lo);
-          fma2(acc[i][1], p2, v0.hi);
-          fma2(acc[i][2], p2, v1.lo);
-          fma2(acc[i][3], p2, v1.hi);
+        for (int tt = t4; tt < t4 + 4; ++tt) {
+          const f32x4 v0 = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 4 * cg);
+          const f32x4 v1 = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 256 + 4 * cg);
+          const float4 pa = *reinterpret_cast<const float4*>(ps + tt * kRows + 8 * rg);
+          const float4 pb = *reinterpret_cast<const float4*>(ps + tt * kRows + 8 * rg + 4);
+          const float pr[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const f32x2 p2 = pack2(pr[i], pr[i]);
+            fma2(acc[i][0], p2, v0.lo);
+            fma2(acc[i][1], p2, v0.hi);
+            fma2(acc[i][2], p2, v1.lo);
+            fma2(acc[i][3], p2, v1.hi);
+          }
         }
       }
     } else {
 #pragma unroll 1
-      for (int tt = 0; tt < kToks; ++tt) {
+      for (int tt = 0; tt < nt; ++tt) {
         const f32x4 v0 = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 4 * cg);
         const f32x4 v1 = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 256 + 4 * cg);
 #pragma unroll
