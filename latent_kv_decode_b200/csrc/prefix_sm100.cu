@@ -52,6 +52,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "once_per_device.h"
 #include "prefix.h"
 #include "sm100_ptx.cuh"
@@ -854,12 +856,15 @@ bool prefix_sm100_supported(const mla_prefix_args* a) {
          }) == cudaSuccess;
 }
 
+// As many clusters as run at once, but no range shorter than a tile of the blocks'
+// most: down to one tile a range the merge costs less than the tiles it spares (16
+// sequences of 8 heads, 500 + 100 tokens: 43, 22, 16 us with 1, 5, 20 ranges).
 int prefix_sm100_auto_splits(const mla_prefix_args* a, int sms) {
-  const int pairs = sms / 2;
-  const int64_t blocks = ((int64_t)a->B * a->H * a->Q + kRowsT - 1) / kRowsT;
-  const int64_t tiles = ((int64_t)a->prefix_len + kTileT - 1) / kTileT + (a->Lk + kTileT - 1) / kTileT;
-  int64_t s = pairs / blocks;
-  if (s > tiles) s = tiles;
+  const int pairs = sms / 2, HQ = a->H * a->Q;
+  const int64_t blocks = ((int64_t)a->B * HQ + kRowsT - 1) / kRowsT;
+  const int64_t seqs = std::min<int64_t>(a->B, (kRowsT + HQ - 1) / HQ);   // of a block
+  const int64_t tiles = ((int64_t)a->prefix_len + kTileT - 1) / kTileT + seqs * ((a->Lk + kTileT - 1) / kTileT);
+  const int64_t s = std::min(pairs / blocks, tiles);
   return s < 1 ? 1 : (int)s;
 }
 
