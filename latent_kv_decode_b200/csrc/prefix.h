@@ -98,6 +98,14 @@ struct TileWalk {
   }
 };
 
+// At most s ranges (1 if less), as few as keep the longest as short: ranges that
+// would be empty or shorter only lengthen the merge.
+inline int even_splits(int64_t tiles, int64_t s) {
+  if (s <= 1 || tiles <= 1) return 1;
+  const int64_t per = (tiles + s - 1) / s;
+  return (int)((tiles + per - 1) / per);
+}
+
 size_t prefix_simt_smem(int D);
 cudaError_t launch_prefix_simt(const PrefixParams& p, bool bf16, cudaStream_t st);
 int prefix_simt_auto_splits(const mla_prefix_args* a, int sms);

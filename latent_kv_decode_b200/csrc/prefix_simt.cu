@@ -388,10 +388,7 @@ int prefix_simt_auto_splits(const mla_prefix_args* a, int sms) {
   const int64_t blocks = (rows + kRows - 1) / kRows;
   const int64_t seqs = std::min<int64_t>(a->B, (kRows + HQ - 1) / HQ);   // of a block
   const int64_t tiles = ((int64_t)a->prefix_len + kToks - 1) / kToks + seqs * ((a->Lk + kToks - 1) / kToks);
-  int64_t s = sms / blocks;
-  if (s > tiles) s = tiles;
-  if (s > 64) s = 64;
-  return s < 1 ? 1 : (int)s;
+  return even_splits(tiles, std::min({sms / blocks, tiles, (int64_t)64}));
 }
 
 cudaError_t launch_prefix_simt(const PrefixParams& p, bool bf16, cudaStream_t st) {

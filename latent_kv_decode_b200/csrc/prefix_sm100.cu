@@ -864,8 +864,7 @@ int prefix_sm100_auto_splits(const mla_prefix_args* a, int sms) {
   const int64_t blocks = ((int64_t)a->B * HQ + kRowsT - 1) / kRowsT;
   const int64_t seqs = std::min<int64_t>(a->B, (kRowsT + HQ - 1) / HQ);   // of a block
   const int64_t tiles = ((int64_t)a->prefix_len + kTileT - 1) / kTileT + seqs * ((a->Lk + kTileT - 1) / kTileT);
-  const int64_t s = std::min(pairs / blocks, tiles);
-  return s < 1 ? 1 : (int)s;
+  return even_splits(tiles, std::min(pairs / blocks, tiles));
 }
 
 cudaError_t launch_prefix_sm100(const PrefixParams& p, cudaStream_t st) {
