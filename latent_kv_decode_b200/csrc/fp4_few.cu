@@ -1,5 +1,5 @@
-// Products of up to 16 tokens with weights held as FP4 entries (mla_fp4_linear's
-// kernel for few tokens; fp4_linear.cu takes more).
+// Products of few tokens, or small ones, with weights held as FP4 entries
+// (mla_fp4_linear; fp4_linear.cu takes the others).
 //
 // Bound: the weights' bytes (0.5625 per element) and, at a few MB, the latency of
 // one launch, one trip to memory and one sum across warps. So there is no first
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(32 * kWarps) fp4_few_kernel(const mla_fp4_line
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int gid = lane >> 2, tig = lane & 3;
   const int g = blockIdx.x / tiles, n0 = (blockIdx.x - g * tiles) * kRows;
-  const int T = a.B * a.Q, entries = a.K / kCkv;
+  const int T = a.B * a.Q, t0 = blockIdx.y * kToks, entries = a.K / kCkv;
 
   const uint8_t* row[2];                     // gid and gid + 8; rows past the last repeat it and are not stored
 #pragma unroll
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(32 * kWarps) fp4_few_kernel(const mla_fp4_line
   const __nv_bfloat16* x[kN];                // likewise tokens past the last: a column of its own each
 #pragma unroll
   for (int j = 0; j < kN; ++j) {
-    const int t = min(8 * j + gid, T - 1);
+    const int t = min(t0 + 8 * j + gid, T - 1);
     x[j] = reinterpret_cast<const __nv_bfloat16*>(a.x) + (int64_t)(t / a.Q) * a.x_batch_stride +
            (int64_t)(t % a.Q) * a.x_token_stride + (int64_t)g * a.x_group_stride + 32 * tig;
   }
@@ -196,8 +196,8 @@ __global__ void __launch_bounds__(32 * kWarps) fp4_few_kernel(const mla_fp4_line
     for (int k = 0; k < 4; ++k) mine[(8 * j + 2 * tig + (k & 1)) * kRows + 8 * (k >> 1) + gid] = acc[j][k];
   __syncthreads();
   const double f = (double)a.scale * 128.0;
-  for (int i = threadIdx.x; i < T * kRows; i += blockDim.x) {
-    const int t = i / kRows, n = n0 + i % kRows;
+  for (int i = threadIdx.x; i < min(kToks, T - t0) * kRows; i += blockDim.x) {
+    const int t = t0 + i / kRows, n = n0 + i % kRows;
     float sum = part[i];
     for (int k = 1; k < warps; ++k) sum += part[k * kToks * kRows + i];
     if (n < a.N)
@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(32 * kWarps) fp4_few_kernel(const mla_fp4_line
 template <int kN>
 cudaError_t launch(const mla_fp4_linear_args* a, int sms, cudaStream_t st) {
   const int tiles = (a->N + kRows - 1) / kRows;
-  const int64_t ctas = (int64_t)a->G * tiles;
+  const int blocks = (a->B * a->Q + 8 * kN - 1) / (8 * kN);
+  const int64_t ctas = (int64_t)a->G * tiles * blocks;
   // The 16 warps that an SM holds go to as many CTAs as it gets, up to four: 11.2,
   // 9.0 and 10.8 us with 16, 8 and 4 warps for 256 CTAs (8192 to 4096, one token),
   // 32.8, 28.1 and 28.0 for 448 (16384 to 7168), 5.5, 6.3 and 9.4 for 96.
@@ -217,7 +218,7 @@ cudaError_t launch(const mla_fp4_linear_args* a, int sms, cudaStream_t st) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.gridDim = dim3((unsigned)(a->G * tiles), (unsigned)blocks);
   cfg.blockDim = dim3((unsigned)(32 * warps));
   cfg.dynamicSmemBytes = (size_t)warps * kRows * 8 * kN * sizeof(float);
   cfg.stream = st;
@@ -230,12 +231,15 @@ cudaError_t launch(const mla_fp4_linear_args* a, int sms, cudaStream_t st) {
 }  // namespace
 
 // This kernel against the other with its two launches, in us: 512 to 200 2.0 : 6.4
-// (one token), 3.3 : 7.1 (16); 7168 to 1536 5.8 : 9.1, 8.0 : 10.2; 8192 to 4096 8.7 :
-// 13.2, 14.2 : 13.6; 16384 to 7168 26.2 : 28.3, at 8 tokens 30.9 : 28.2. Every 16 rows
-// read all activations again, so the limit is on tokens x weights.
+// (one token), 3.3 : 12.0 (64); 4096 to 1000 5.1 : 8.4 (16), 8.1 : 11.0 (64), 13.5 : 12.1
+// (96); 7168 to 1536 5.8 : 9.1 (1), 8.0 : 10.2 (16), 12.1 : 10.3 (24); 8192 to 4096 8.9 :
+// 13.2 (1), 10.5 : 13.4 (8), 14.4 : 13.6 (16); 16384 to 7168 26.2 : 28.3 (1), 30.9 : 28.2
+// (8). Every 16 tokens read all weights again and every 16 rows all activations, so
+// the limits are on tokens x weights, and on the weights where they are read twice.
 bool fp4_few_tokens(const mla_fp4_linear_args* a) {
-  const int64_t T = (int64_t)a->B * a->Q;
-  return T <= 16 && (int64_t)a->G * a->N * a->K <= ((int64_t)1 << 29) / T;   // G*N is at most 2^30
+  // G*N is at most 2^30; K is at least 512, so a grid dimension holds the blocks of tokens
+  const int64_t tokens = (int64_t)a->B * a->Q, weights = (int64_t)a->G * a->N * a->K;
+  return weights <= ((int64_t)1 << 28) / tokens && (tokens <= 16 || weights <= 1 << 23);
 }
 
 cudaError_t launch_fp4_few(const mla_fp4_linear_args* a, int sms, cudaStream_t st) {

@@ -1,5 +1,5 @@
 // Products of few tokens with weights held as FP4 entries (mla_fp4_linear); the
-// fewest tokens go to fp4_few.cu's kernel.
+// fewest tokens, and small products, go to fp4_few.cu's kernel.
 //
 // The weights are the bytes: 0.5625 per element, read once per 64 tokens. What
 // it takes to stream them is to turn 4-bit codes into tensor-core operands as

@@ -159,8 +159,8 @@ def test_fp4_linear_rejects(L, over, status):
 
 
 def test_fp4_linear_workspace(L):
-    assert L.mla_fp4_linear_workspace_size(ctypes.byref(_linear())) == 0     # few tokens need none
-    a = _linear(B=12)
+    assert L.mla_fp4_linear_workspace_size(ctypes.byref(_linear())) == 0     # small products need none
+    a = _linear(B=12, N=4096)
     need = L.mla_fp4_linear_workspace_size(ctypes.byref(a))
     assert need == 24 * 4 * 1024 * 2 + 24 * 4 * 4        # float16 activations, an exponent per token and group
     assert L.mla_fp4_linear(ctypes.byref(a), None, 0, None) == 3

@@ -69,6 +69,42 @@ def test_few_tokens_with_many_entries_and_rows(T, N, K):
     assert torch.equal(ops.mla_fp4_linear(x[-1:].cuda(), w.cuda(), 0.01)[0], y[-1])
 
 
+@pytest.mark.parametrize("T", [25, 33, 64, 65, 130])
+@pytest.mark.parametrize("N,K", [(21600, 512), (5001, 2560), (1300, 8704)])
+def test_larger_products(T, N, K):
+    """Ragged token and row blocks, one, five and seventeen entries a row."""
+    from latent_kv_decode_b200 import ops
+    w = _entries((N, K // 512), seed=N + 1)
+    x = torch.randn(T, K, generator=torch.Generator().manual_seed(T + 30)).bfloat16()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = ops.mla_fp4_linear(x.cuda(), w.cuda(), 0.013, err_flag=err)
+    assert int(err.item()) == 0
+    _check(y, x.double(), _values(w), 0.013)
+
+
+def test_magnitudes_and_bad_values_of_larger_products():
+    # as the tests of small products, with enough rows for the other kernel
+    from latent_kv_decode_b200 import ops
+    w = _entries((11000, 2), seed=3)
+    base = torch.randn(26, 1024, generator=torch.Generator().manual_seed(4)).bfloat16()
+    for k, p in enumerate([-126, -100, -30, 0, 30, 100, 115]):
+        base[k] = (base[k].double() * 2.0 ** p).bfloat16()
+    base[7, ::2] = 0
+    base[8] = 0
+    v = _values(w)
+    good = ops.mla_fp4_linear(base.cuda(), w.cuda(), 2.0 ** -16)
+    _check(good, base.double(), v, 2.0 ** -16)
+    assert (good[8] == 0).all()
+    base[11, 7], base[13, 9] = math.nan, math.inf
+    y = ops.mla_fp4_linear(base.cuda(), w.cuda(), 2.0 ** -16)
+    assert torch.isnan(y[11]).all()
+    want = torch.where(v[:, 9] == 0, torch.full_like(v[:, 9], math.nan), v[:, 9] * math.inf)
+    assert torch.equal(torch.nan_to_num(y[13].cpu().double(), nan=7.0, posinf=8.0, neginf=9.0),
+                       torch.nan_to_num(want, nan=7.0, posinf=8.0, neginf=9.0))
+    rest = [t for t in range(26) if t not in (11, 13)]
+    assert torch.equal(y[rest], good[rest])
+
+
 @pytest.mark.parametrize("p", [-130, -126, -100, -30, 30, 100, 115])
 def test_one_token_over_bf16s_whole_range(p):
     from latent_kv_decode_b200 import ops
