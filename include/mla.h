@@ -424,9 +424,10 @@ mla_status_t mla_rope_append(const mla_rope_append_args* a, void* stream);
  *     anything, NaN included.
  *   sinks: as for mla_decode.
  *   Supported: MLA_F32 or MLA_BF16; Ckv = 512; Dr 0, 32 or 64; H a multiple of 8
- *     up to 128, Q 1..4; B*H*Q up to 2^24, prefix_len + Lk up to 2^30. bf16 with contiguous storage or pages of a
- *     multiple of 64 rows runs on the tensor cores; everything else in float32
- *     on the CUDA cores.
+ *     up to 128, Q 1..4; B*H*Q up to 2^24, prefix_len + Lk up to 2^30. bf16 with
+ *     contiguous storage or pages of a multiple of 64 rows runs at the tensor
+ *     cores' full rate; everything else in float32 precision (six products of
+ *     bf16 parts each).
  *   num_splits: 0 = auto; each block of stacked rows cuts its tokens into this
  *     many ranges, and the call then merges the partial results itself (no
  *     mla_combine): x and lse are final when the enqueued work completes.

@@ -106,7 +106,6 @@ inline int even_splits(int64_t tiles, int64_t s) {
   return (int)((tiles + per - 1) / per);
 }
 
-size_t prefix_simt_smem(int D);
 cudaError_t launch_prefix_simt(const PrefixParams& p, bool bf16, cudaStream_t st);
 int prefix_simt_auto_splits(const mla_prefix_args* a, int sms);
 

@@ -1,18 +1,21 @@
-// Shared-prefix decode on the CUDA cores, in float32: the path of float32
-// inputs (which need full precision) and of page sizes that the tensor-core
-// kernel does not take.
+// Shared-prefix decode in float32, without tensor memory: the path of float32 inputs
+// and of page sizes that the other kernel does not take.
 //
 // A CTA owns 32 stacked rows and a range of their 16-token tiles, two of which
 // are in flight: the next tile's rows arrive (cp.async) while this one computes.
-//   S = Q . K^T    sixteen groups of 16 threads take a sixteenth of the 576-wide
-//                  dot each, 8 x 4 scores per thread; the parts are summed by the
-//                  softmax.
+//   S = Q . K^T    a warp sums every eighth 16 channels for all rows and tokens; the
+//                  parts are summed by the softmax.
 //   softmax        warp w keeps the online statistics of rows 4w .. 4w+3, two at
 //                  a time, a lane per token.
-//   O += P . V     thread = 8 rows x 8 columns of the 32 x 512 accumulator.
-// Both products are packed float32 FMAs. What bounds them is what shared memory
-// returns to registers, 32 floats a clock and SM: S reads 24 floats for 64 FMA,
-// O 16 (tiles of 4 x 2 and 8 x 4 took 2.5 + 2.1 us a tile instead of 2.4 + 1.5).
+//   O += P . V     a warp owns 64 of the 512 columns.
+// The products are mma.m16n8k16 on bf16 parts: a float32 value is the sum of three
+// bf16, exactly (down to their smallest, 2^-133), and of the nine products of two such sums the six largest count
+// (the others are below 2^-25 of the first), added in float32. Q is split once per
+// CTA, K and V as their fragments are read, the weights by the softmax. Measured: 4.1
+// us a tile (S 1.5, softmax 0.8, O 1.1), where packed float32 FMAs, which shared
+// memory feeds with 32 floats a clock, took 5.4; 128 rows behind 2049 tokens 39 -> 31
+// us. (The warp-level instruction, as its operands come from registers, split there;
+// for tcgen05 the parts would have to be written to shared memory in its layout.)
 //
 // Tokens that no row may see are zeros in the tile, so whatever their cache
 // rows hold stays out of the sums; where a tile that some rows do not see holds
@@ -27,27 +30,48 @@ namespace mla {
 namespace {
 
 constexpr int kRows = 32, kToks = 16;
-constexpr int kThr = 256, kWarps = kThr / 32, kParts = kThr / 16;   // kParts slices of the dot product
-constexpr int kPad = 4;             // floats of row padding: 16-byte rows, 8 rows over all banks
+constexpr int kThr = 256, kWarps = kThr / 32, kParts = kWarps;   // kParts slices of the dot product
+constexpr int kPad = 8;             // floats of row padding: four rows x eight floats cover the banks
 constexpr int kPart = kToks + 1;
+constexpr float kTop = 3.3895313892515355e38f;   // bf16's largest
+constexpr int kProw = kToks / 2 + 4;             // 32-bit words of a row of weights
 
 __host__ __device__ constexpr int pitch_of(int D) { return D + kPad; }
+__host__ __device__ constexpr int qpitch_of(int D) { return D / 2 + 4; }     // words of a query row's piece
 
-using f32x2 = unsigned long long;                // two floats, the first in the low half
-struct alignas(16) f32x4 { f32x2 lo, hi; };
+// bf16 pieces of a float32 operand: x = piece 0 + piece 1 + piece 2 exactly (a bf16
+// operand is its own piece). Two weights in [0, 1] of bf16 values need two.
+template <typename T> constexpr int kPieces = sizeof(T) == 4 ? 3 : 1;
+template <typename T> constexpr int kWPieces = sizeof(T) == 4 ? 3 : 2;
 
-__device__ __forceinline__ void fma2(f32x2& acc, f32x2 a, f32x2 b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+// The pieces of a pair, the first value in the low halves. Each is the rest's nearest
+// bf16, so a piece is at most 2^-9 of the one before it.
+template <int kP> __device__ __forceinline__ void split(float x, float y, uint32_t (&p)[kP]) {
+#pragma unroll
+  for (int i = 0; i < kP; ++i) {
+    p[i] = sm100::pack_bf16(x, y);
+    x -= __uint_as_float(p[i] << 16);
+    y -= __uint_as_float(p[i] & 0xffff0000u);
+  }
 }
-__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
+
+// The pieces of a query value that is not below bf16's largest: that first, then the
+// rest; a non-finite value is its own first piece.
+template <int kP> __device__ __forceinline__ void split_large(float x, uint16_t (&p)[kP]) {
+  const bool finite = isfinite(x);
+#pragma unroll
+  for (int i = 0; i < kP; ++i) {
+    const float h = i > 0 ? (finite ? x : 0.f) : finite ? fminf(fmaxf(x, -kTop), kTop) : x;
+    p[i] = (uint16_t)sm100::pack_bf16(h, h);
+    x -= __uint_as_float((uint32_t)p[i] << 16);
+  }
 }
-__device__ __forceinline__ float2 unpack2(f32x2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // 16 bytes from global to shared memory, or zeros
@@ -59,6 +83,9 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool ok) {
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int n> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory"); }
 
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
   const uint2 u = *reinterpret_cast<const uint2*>(p);
   return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
@@ -102,11 +129,13 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
   __shared__ const T* row_lat[2][kToks];         // the tile's cache rows, null where no row may see the token
   __shared__ const T* row_pe[2][kToks];
   const int D = p.D, pitch = pitch_of(D);
-  float* qs = smem;                              // [kRows][pitch]
-  float* ks = qs + kRows * pitch;                // [2][kToks][pitch]
+  constexpr int kP = kPieces<T>, kWP = kWPieces<T>;
+  const int qpitch = qpitch_of(D);
+  uint32_t* qs = reinterpret_cast<uint32_t*>(smem);             // [kP][kRows][qpitch] pairs of channels
+  float* ks = smem + kP * kRows * qpitch;        // [2][kToks][pitch]
   float* part = ks + 2 * kToks * pitch;          // [kParts][kRows][kPart] parts of the scores
-  float* ps = part + kParts * kRows * kPart;     // [kToks][kRows] weights
-  float* alpha = ps + kToks * kRows;             // [kRows]
+  uint32_t* ps = reinterpret_cast<uint32_t*>(part + kParts * kRows * kPart);   // [kWP][kRows][kProw] weights
+  float* alpha = reinterpret_cast<float*>(ps + kWP * kRows * kProw);           // [kRows]
   float* stat = alpha + kRows;                   // [kRows] 1 / denominator
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -114,6 +143,17 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
   sm100::pdl_wait();
   const int r0 = blockIdx.x * kRows, z = blockIdx.y;
   const int nr = min(kRows, p.N - r0);
+  const T* q_lat = reinterpret_cast<const T*>(p.q_lat) + (int64_t)r0 * p.Ckv;
+  const T* q_pe = reinterpret_cast<const T*>(p.q_pe) + (int64_t)r0 * p.Dr;
+  float4 q[kRows / kWarps][5];                   // the query rows, before anything waits
+#pragma unroll
+  for (int h = 0; h < kRows / kWarps; ++h)
+#pragma unroll
+    for (int u = 0; u < 5; ++u) {
+      const int r = warp + h * kWarps, k = 4 * (lane + 32 * u);
+      q[h][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < nr && k < D) q[h][u] = load4(k < kCkv ? q_lat + (int64_t)r * kCkv + k : q_pe + (int64_t)r * p.Dr + (k - kCkv));
+    }
   const int b0 = r0 / p.HQ, b1 = (r0 + nr - 1) / p.HQ;
   __shared__ int lens[kRows / 8 + 1];            // H*Q >= 8: the sequences a block can hold rows of
   if (tid <= b1 - b0) lens[tid] = prefix_len_of(p, b0 + tid);
@@ -121,11 +161,6 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
   const int tiles = TileWalk<kToks>::count(p, lens, b0, b1);
   const int per = (tiles + p.num_splits - 1) / p.num_splits;
   const int j0 = min(tiles, z * per), j1 = min(tiles, j0 + per);
-
-  const T* q_lat = reinterpret_cast<const T*>(p.q_lat) + (int64_t)r0 * p.Ckv;
-  const T* q_pe = reinterpret_cast<const T*>(p.q_pe) + (int64_t)r0 * p.Dr;
-  load_rows<T, kRows>(qs, D, [&](int r) { return r < nr ? q_lat + (int64_t)max(r, 0) * p.Ckv : nullptr; },
-                      [&](int r) { return q_pe + (int64_t)r * p.Dr; });
 
   // the rows of tile `w` into buffer s (after a barrier that follows its last use)
   auto locate = [&](const TileWalk<kToks>& w, int s) {
@@ -165,9 +200,37 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
   }
   copy_commit();
 
-  // S: thread (ty, tx) of part kq holds rows ty + 4i, tokens tx + 4n
-  const int kq = tid >> 4, ty = (tid >> 2) & 3, tx = tid & 3;
-  const int kn = D / kParts;                     // channels per part, even (D is a multiple of 32)
+  // the query rows as pieces, while the first tile arrives
+  bool large = false;
+#pragma unroll
+  for (int h = 0; h < kRows / kWarps; ++h)
+#pragma unroll
+    for (int u = 0; u < 5; ++u) {
+      const int r = warp + h * kWarps, k = 4 * (lane + 32 * u);
+      if (k >= D) continue;
+      const float4 v = q[h][u];
+      large = large || !(fabsf(v.x) < kTop && fabsf(v.y) < kTop && fabsf(v.z) < kTop && fabsf(v.w) < kTop);
+      uint32_t lo[kP], hi[kP];
+      split<kP>(v.x, v.y, lo);
+      split<kP>(v.z, v.w, hi);
+#pragma unroll
+      for (int c = 0; c < kP; ++c)
+        *reinterpret_cast<uint2*>(qs + (c * kRows + r) * qpitch + k / 2) = make_uint2(lo[c], hi[c]);
+    }
+  if (large) {
+    for (int r = warp; r < nr; r += kWarps)
+      for (int k = 4 * lane; k < D; k += 128)
+        for (int e = 0; e < 4; ++e) {            // this thread's values once more
+          const float v = load1(k < kCkv ? q_lat + (int64_t)r * kCkv + k + e : q_pe + (int64_t)r * p.Dr + (k - kCkv) + e);
+          if (fabsf(v) < kTop) continue;
+          uint16_t x[kP];
+          split_large<kP>(v, x);
+          for (int c = 0; c < kP; ++c) reinterpret_cast<uint16_t*>(qs + (c * kRows + r) * qpitch)[k + e] = x[c];
+        }
+  }
+
+  // S: a warp sums every eighth 16 channels
+  const int gid = lane >> 2, tig = lane & 3;
   // softmax: rows 4 warp + 2i + lane / 16, token lane % 16
   const int sub = lane >> 4, tok = lane & 15;
   float m_run[2], l_run[2];
@@ -181,11 +244,12 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
     row_lim[i] = 0x7fffffff;
     if (r < p.N && p.causal) row_lim[i] = lens[row_b[i] - b0] - p.Q + r % p.Q;
   }
-  // O: rows 8 rg + i, columns 4 cg + k and 256 + 4 cg + k
-  const int rg = tid >> 6, cg = tid & 63;
-  f32x2 acc[8][4];
+  // O: rows 16 m + 8 (k / 2) + gid, columns 64 warp + 8 n + 2 tig + k % 2
+  float acc[2][8][4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0ull;
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int n = 0; n < 8; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
 
   for (int j = j0; j < j1; ++j) {
     const int buf = (j - j0) & 1;
@@ -199,31 +263,67 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
     const bool pre = w.b < 0;
     bool odd = false;                            // a non-finite score: a non-finite key
     {
-      f32x2 s[8][4] = {};                          // sums over even and odd channels
-      const float* qp = qs + ty * pitch + kq * kn;
-      const float* kp = kt + tx * pitch + kq * kn;
-#pragma unroll 2
-      for (int k = 0; k < kn; k += 2) {
-        f32x2 qv[8], kv[4];
+      float c[2][2][4] = {};                     // [16 rows][8 tokens]
+      for (int k = 16 * warp; k < D; k += 16 * kParts) {
+        uint32_t qa[2][kP][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) qv[i] = *reinterpret_cast<const f32x2*>(qp + 4 * i * pitch + k);
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int n = 0; n < 4; ++n) kv[n] = *reinterpret_cast<const f32x2*>(kp + 4 * n * pitch + k);
+          for (int i = 0; i < kP; ++i) {
+            const uint32_t* a = qs + (i * kRows + 16 * m + gid) * qpitch + k / 2 + tig;
+            qa[m][i][0] = a[0];
+            qa[m][i][1] = a[8 * qpitch];
+            qa[m][i][2] = a[4];
+            qa[m][i][3] = a[8 * qpitch + 4];
+          }
+        uint32_t kb[2][2][kP];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int n = 0; n < 4; ++n) fma2(s[i][n], qv[i], kv[n]);
+          for (int h = 0; h < 2; ++h) {
+            const float2 v = *reinterpret_cast<const float2*>(kt + (8 * n + gid) * pitch + k + 8 * h + 2 * tig);
+            split<kP>(v.x, v.y, kb[n][h]);
+          }
+        // products of pieces down to 2^-18 of the first; the others are below 2^-25
+#pragma unroll
+        for (int sum = kP - 1; sum >= 0; --sum)
+#pragma unroll
+          for (int i = 0; i <= sum; ++i)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int n = 0; n < 2; ++n) mma16816(c[m][n], qa[m][i], kb[n][0][sum - i], kb[n][1][sum - i]);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const float2 v = unpack2(s[i][n]);
-          part[(kq * kRows + ty + 4 * i) * kPart + tx + 4 * n] = v.x + v.y;
-          odd = odd || !isfinite(v.x + v.y);
-        }
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            part[(warp * kRows + 16 * m + 8 * (k >> 1) + gid) * kPart + 8 * n + 2 * tig + (k & 1)] = c[m][n][k];
+            odd = odd || !isfinite(c[m][n][k]);
+          }
     }
     const bool any_odd = __syncthreads_or(odd);
+    if (any_odd) {
+      // an infinity's pieces are no sum: the tile's scores once more, channel by channel
+      for (int i = tid; i < kRows * kToks; i += kThr) {
+        const int r = i / kToks, t = i % kToks;
+        float v = 0.f;
+        for (int k = 0; k < D; ++k) {
+          float q = 0.f;
+#pragma unroll
+          for (int c = kP - 1; c >= 0; --c) {
+            const uint32_t u = qs[(c * kRows + r) * qpitch + k / 2];
+            q += __uint_as_float(k & 1 ? u & 0xffff0000u : u << 16);
+          }
+          v = fmaf(q, kt[t * pitch + k], v);
+        }
+#pragma unroll
+        for (int c = 0; c < kParts; ++c) part[(c * kRows + r) * kPart + t] = c ? 0.f : v;
+      }
+      __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int srow = 4 * warp + 2 * i + sub;
@@ -247,54 +347,79 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
       for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       l_run[i] = l_run[i] * al + sum;
       m_run[i] = m_new;
-      ps[tok * kRows + srow] = e;
+      // tokens t, t + 4, t + 8, t + 12 are an MMA's K positions 2t, 2t + 1, 2t + 8, 2t + 9
+      const int pos = ((tok >> 3) << 3) + 2 * (tok & 3) + ((tok >> 2) & 1);
+      float rest = e;
+#pragma unroll
+      for (int c = 0; c < kWP; ++c) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(rest);
+        reinterpret_cast<__nv_bfloat16*>(ps + (c * kRows + srow) * kProw)[pos] = h;
+        rest -= __bfloat162float(h);
+      }
       if (tok == 0) alpha[srow] = al;
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float al = alpha[8 * rg + i];
-      const f32x2 al2 = pack2(al, al);
+    for (int m = 0; m < 2; ++m) {
+      const float al0 = alpha[16 * m + gid], al1 = alpha[16 * m + 8 + gid];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(acc[i][k]) : "l"(al2));
+      for (int n = 0; n < 8; ++n) {
+        acc[m][n][0] *= al0;
+        acc[m][n][1] *= al0;
+        acc[m][n][2] *= al1;
+        acc[m][n][3] *= al1;
+      }
     }
-    const int nt = min(kToks, w.end - w.t);      // tokens past it have no weight
+    const float* vt = kt + 64 * warp;
     if (!any_odd) {
-#pragma unroll 1
-      for (int t4 = 0; t4 < nt; t4 += 4) {
+      uint32_t pa[2][kWP][4];
 #pragma unroll
-        for (int tt = t4; tt < t4 + 4; ++tt) {
-          const f32x4 v0 = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 4 * cg);
-          const f32x4 v1 = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 256 + 4 * cg);
-          const float4 pa = *reinterpret_cast<const float4*>(ps + tt * kRows + 8 * rg);
-          const float4 pb = *reinterpret_cast<const float4*>(ps + tt * kRows + 8 * rg + 4);
-          const float pr[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const f32x2 p2 = pack2(pr[i], pr[i]);
-            fma2(acc[i][0], p2, v0.lo);
-            fma2(acc[i][1], p2, v0.hi);
-            fma2(acc[i][2], p2, v1.lo);
-            fma2(acc[i][3], p2, v1.hi);
-          }
+        for (int c = 0; c < kWP; ++c) {
+          const uint32_t* q = ps + (c * kRows + 16 * m + gid) * kProw + tig;
+          pa[m][c][0] = q[0];
+          pa[m][c][1] = q[8 * kProw];
+          pa[m][c][2] = q[4];
+          pa[m][c][3] = q[8 * kProw + 4];
         }
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const float* v = vt + tig * pitch + 8 * n + gid;
+        uint32_t v0[kP], v1[kP];
+        split<kP>(v[0], v[4 * pitch], v0);
+        split<kP>(v[8 * pitch], v[12 * pitch], v1);
+#pragma unroll
+        for (int sum = kWP - 1; sum >= 0; --sum)
+#pragma unroll
+          for (int i = 0; i < kP; ++i)
+            if (sum - i >= 0)
+#pragma unroll
+              for (int m = 0; m < 2; ++m) mma16816(acc[m][n], pa[m][sum - i], v0[i], v1[i]);
       }
     } else {
+      // rows whose weight is 0 skip the token
 #pragma unroll 1
-      for (int tt = 0; tt < nt; ++tt) {
-        const f32x4 v0 = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 4 * cg);
-        const f32x4 v1 = *reinterpret_cast<const f32x4*>(kt + tt * pitch + 256 + 4 * cg);
+      for (int t = 0; t < kToks; ++t) {
+        const int pos = ((t >> 3) << 3) + 2 * (t & 3) + ((t >> 2) & 1);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float pr = ps[tt * kRows + 8 * rg + i];
-          if (pr != 0.f) {
-            const f32x2 p2 = pack2(pr, pr);
-            fma2(acc[i][0], p2, v0.lo);
-            fma2(acc[i][1], p2, v0.hi);
-            fma2(acc[i][2], p2, v1.lo);
-            fma2(acc[i][3], p2, v1.hi);
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float pr = 0.f;
+#pragma unroll
+            for (int c = kWP - 1; c >= 0; --c)
+              pr += __bfloat162float(
+                  reinterpret_cast<const __nv_bfloat16*>(ps + (c * kRows + 16 * m + 8 * h + gid) * kProw)[pos]);
+            if (pr != 0.f) {
+#pragma unroll
+              for (int n = 0; n < 8; ++n) {
+                const float2 v = *reinterpret_cast<const float2*>(vt + t * pitch + 8 * n + 2 * tig);
+                acc[m][n][2 * h] = fmaf(pr, v.x, acc[m][n][2 * h]);
+                acc[m][n][2 * h + 1] = fmaf(pr, v.y, acc[m][n][2 * h + 1]);
+              }
+            }
           }
-        }
       }
     }
     w = wn;
@@ -302,7 +427,7 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
   }
 
   // the rows' denominators to the accumulator's threads
-  const bool split = p.num_splits > 1;
+  const bool parts = p.num_splits > 1;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -311,7 +436,7 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
     float inv = 0.f;
     if (r < p.N) {
       float wt = 1.f;
-      if (!split && p.sinks) {
+      if (!parts && p.sinks) {
         const float sk = p.sinks[(r % p.HQ) / p.Q], m2 = fmaxf(m, sk);
         wt = m == -INFINITY ? 0.f : expf(m - m2);
         l = l * wt + expf(sk - m2);
@@ -321,7 +446,7 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
       inv = seen ? wt / l : 0.f;
       const float lse = seen ? m + logf(l) : -INFINITY;
       if (tok == 0) {
-        if (split)
+        if (parts)
           p.ws_lse[(int64_t)z * p.N + r] = lse;
         else if (p.lse)
           p.lse[r] = lse;
@@ -331,33 +456,39 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = r0 + 8 * rg + i;
-    if (r >= p.N) continue;
-    const float inv = stat[8 * rg + i];
+  for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int c = 256 * k + 4 * cg;
-      const float2 lo = unpack2(acc[i][2 * k]), hi = unpack2(acc[i][2 * k + 1]);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (inv != 0.f) v = make_float4(lo.x * inv, lo.y * inv, hi.x * inv, hi.y * inv);
-      if (split)
-        *reinterpret_cast<float4*>(p.ws_o + ((int64_t)z * p.N + r) * p.Ckv + c) = v;
-      else if constexpr (sizeof(T) == 4)
-        *reinterpret_cast<float4*>(reinterpret_cast<T*>(p.x) + (int64_t)r * p.Ckv + c) = v;
-      else
-        *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.x) + (int64_t)r * p.Ckv + c) =
-            make_uint2(sm100::pack_bf16(v.x, v.y), sm100::pack_bf16(v.z, v.w));
+    for (int h = 0; h < 2; ++h) {
+      const int r = r0 + 16 * m + 8 * h + gid;
+      if (r >= p.N) continue;
+      const float inv = stat[r - r0];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const int c = 64 * warp + 8 * n + 2 * tig;
+        float2 v = make_float2(0.f, 0.f);
+        if (inv != 0.f) v = make_float2(acc[m][n][2 * h] * inv, acc[m][n][2 * h + 1] * inv);
+        if (parts)
+          *reinterpret_cast<float2*>(p.ws_o + ((int64_t)z * p.N + r) * p.Ckv + c) = v;
+        else if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<float2*>(reinterpret_cast<T*>(p.x) + (int64_t)r * p.Ckv + c) = v;
+        else
+          *reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(p.x) + (int64_t)r * p.Ckv + c) = sm100::pack_bf16(v.x, v.y);
+      }
     }
-  }
+}
+
+template <typename T>
+constexpr size_t smem_bytes(int D) {
+  return 4 * ((size_t)kPieces<T> * kRows * qpitch_of(D) + 2 * kToks * pitch_of(D) + kParts * kRows * kPart +
+              kWPieces<T> * kRows * kProw + 2 * kRows);
 }
 
 template <typename T>
 cudaError_t launch(const PrefixParams& p, cudaStream_t st) {
-  const size_t smem = prefix_simt_smem(p.D);
+  const size_t smem = smem_bytes<T>(p.D);
   static OncePerDevice smem_set;
   cudaError_t e = smem_set([] {
-    return cudaFuncSetAttribute(prefix_simt<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prefix_simt_smem(kCkv + 64));
+    return cudaFuncSetAttribute(prefix_simt<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<T>(kCkv + 64));
   });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -376,12 +507,8 @@ cudaError_t launch(const PrefixParams& p, cudaStream_t st) {
 
 }  // namespace
 
-size_t prefix_simt_smem(int D) {
-  return sizeof(float) * ((size_t)(kRows + 2 * kToks) * pitch_of(D) + kParts * kRows * kPart + kToks * kRows + 2 * kRows);
-}
-
 // About one CTA per SM (its shared memory fills one), no split shorter than a
-// tile: a tile takes 5.4 us, the merge of a few splits 3.
+// tile: a tile takes 4.1 us, the merge of a few splits 3.
 int prefix_simt_auto_splits(const mla_prefix_args* a, int sms) {
   const int HQ = a->H * a->Q;
   const int64_t rows = (int64_t)a->B * HQ;

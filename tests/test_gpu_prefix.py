@@ -316,6 +316,47 @@ def test_references_that_start_and_move_in_either_half_of_a_block(Lp, splits):
     assert (x.cpu()[~fin] == 0).all() and (lse.cpu()[~fin] == -math.inf).all()
 
 
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("power", [-90, 0, 90])
+def test_float32_products_keep_float32s_precision(power, page):
+    # one token, one channel of the scores: lse is a single product times the scale. Its
+    # operands' parts add up exactly, six products of parts are added (2^-23 each), what
+    # is left out is below 3 * 2^-25, and the scale rounds once: 8 * 2^-23 of the value
+    d = _case(5, 24, 1, 64, 1, [0] * 5, dtype=torch.float32, page=page, seed=23)
+    ch = 37
+    q = d["q_lat"]
+    q[..., ch] *= 2.0 ** power
+    if power > 0:
+        q[0, 0, 0, ch], q[1, 2, 0, ch] = 3.4e38, -3.3961e38            # beyond bf16's largest value
+    d["q_pe"].zero_()
+    row = d["pkv"][d["prefix_table"][0].item()][0] if page else d["pkv"][0]
+    k = row[ch].item() * 2.0 ** -power
+    rest = torch.zeros_like(row)
+    rest[ch] = k
+    row.copy_(rest)
+    x, lse, err = _run(d)
+    assert err == 0
+    want = q[..., ch].double() * float(row[ch]) * d["scale"]
+    # the call's scale is float32: half a step of it more
+    assert ((lse.cpu().double() - want).abs() <= 9 * 2.0 ** -23 * want.abs()).all()
+    # the only token's weight is 1
+    assert ((x.cpu() - row.cpu()).abs() <= 3 * 2.0 ** -23 * row.abs().cpu()).all()
+
+
+def test_float32_rows_with_a_non_finite_query():
+    d = _case(3, 16, 1, 64, 40, [5, 6, 7], dtype=torch.float32, seed=24)
+    good = _run(d)
+    d["q_lat"][1, 3, 0, 5] = math.inf
+    d["q_lat"][2, 4, 0, 6] = math.nan
+    x, lse, err = _run(d)
+    hit = torch.zeros(3, 16, dtype=torch.bool)
+    hit[1, 3] = hit[2, 4] = True
+    assert torch.isnan(x[:, :, 0].cpu()[hit]).all() and torch.isfinite(x[:, :, 0].cpu()[~hit]).all()
+    xo, lo, _ = _oracle(d)
+    assert ((x[:, :, 0].cpu().double() - xo[:, :, 0])[~hit].abs() <= 1e-4).all()
+    assert ((good[0] - x)[:, :, 0].cpu()[~hit].abs() <= 2e-4).all()
+
+
 def test_strided_rows_and_separate_storage():
     d = _case(4, 16, 1, 64, 300, [3, 70, 128, 1], pad=64, seed=15)            # 640-wide rows
     _check(d)
