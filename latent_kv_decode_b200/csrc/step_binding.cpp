@@ -200,7 +200,8 @@ OptTensor rope_append(const Tensor& c_kv, const Tensor& k_pe, const Tensor& kv_c
   a.rope_theta = (float)rope_theta;
   a.err_flag = const_cast<int32_t*>(int32_ptr(err_flag, "err_flag"));
   check_status(mla_rope_append(&a, call.handle()), "mla_rope_append");
-  call.used({&q_out});
+  const OptTensor c_kv_o(c_kv);
+  call.used({&c_kv_o, &k_pe_o, &kv_o, &pe_o, &lens_o, &q_pe, &q_out, &cu_tokens, &block_table, &err_flag});
   return q_out;
 }
 
@@ -368,8 +369,8 @@ void fp4_launch(mla_fp4_linear_args& a, const Tensor& x, const Tensor& w, double
   OptTensor ws;
   if (bytes > 0) ws = at::empty({(int64_t)bytes}, x.options().dtype(at::kByte));
   check_status(mla_fp4_linear(&a, ptr(ws), bytes, call.handle()), "mla_fp4_linear");
-  const OptTensor xo(x), oo(out);
-  call.used({&xo, &oo, &ws});
+  const OptTensor xo(x), wo(w), oo(out);
+  call.used({&xo, &wo, &oo, &ws, &err_flag});
 }
 
 bool off16(const Tensor& t) { return reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 != 0; }

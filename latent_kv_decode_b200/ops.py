@@ -590,6 +590,9 @@ def mla_prefix_decode_step(q_nope, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cach
             out = mla_prefix_decode_step(q_nope, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, wkv_b, softmax_scale,
                                          causal_mask, **kw)
         out.record_stream(torch.cuda.current_stream(q_nope.device))
+        for t in (q_nope, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, wkv_b, causal_mask, *kw.values()):
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(s)
         return out
     with torch.cuda.device(q_nope.device):
         q_lat = mla_absorb_q(q_nope, wkv_b)

@@ -224,3 +224,48 @@ def test_refusals_of_the_prefix_decode():
     for kw in bad:
         with pytest.raises(ops.MlaError):
             call(**kw)
+
+
+def test_tensors_dropped_while_another_stream_still_reads_them():
+    # inputs made on the current stream, a call on another that has not reached them
+    # yet, the inputs dropped and their memory asked for again
+    from latent_kv_decode_b200 import ops
+    g = torch.Generator("cuda").manual_seed(31)
+    rnd = lambda *sh: torch.randn(sh, generator=g, device="cuda").bfloat16()
+    B, H, Lk = 8, 16, 128
+    c_kv, k_pe, q_pe = rnd(B, 1, 512), rnd(B, 1, 64), rnd(B, 1, H, 64)
+    lens = torch.full((B,), 5, dtype=torch.int32, device="cuda")
+    q_lat, q_rot, rows = rnd(B, H, 1, 512), rnd(B, H, 1, 64), rnd(700, 576)
+    x = rnd(40, 2048)
+    w = torch.randint(0, 120, (300, 4, 288), generator=g, device="cuda", dtype=torch.uint8)
+    originals = (c_kv, k_pe, q_pe, lens, q_lat, q_rot, rows, x, w)
+
+    def late(stream):
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(20_000_000)
+        return stream
+
+    def append(stream=None):
+        kv, pe = (torch.zeros((B, Lk, n), dtype=torch.bfloat16, device="cuda") for n in (512, 64))
+        a = [t.clone() for t in (c_kv, k_pe, lens, q_pe)]
+        return ops.mla_rope_append(a[0], a[1], kv, pe, a[2], q_pe=a[3], stream=late(stream)), kv, pe
+
+    def decode(stream=None):
+        a = [t.clone() for t in (q_lat, q_rot, rows)]
+        return ops.mla_prefix_decode(a[0], a[1], a[2][:, :512], a[2][:, 512:], None, None, 0.07, stream=late(stream))
+
+    def product(stream=None):
+        a = [t.clone() for t in (x, w)]
+        return (ops.mla_fp4_linear(a[0], a[1], 0.01, stream=late(stream)),)
+
+    s = torch.cuda.Stream()
+    for call in (append, decode, product):
+        want = call()
+        torch.cuda.synchronize()
+        got = call(s)
+        junk = [torch.full_like(t, 7) for t in originals for _ in range(3)]    # where the dropped inputs were
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), call.__name__
+        del junk
