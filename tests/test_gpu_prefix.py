@@ -189,7 +189,7 @@ def test_rope_widths(Dr, dtype):
     _check(_case(4, 16, 1, Dr, 200, [3, 130, 0, 64], dtype=dtype, seed=Dr))
 
 
-@pytest.mark.parametrize("splits", [1, 2, 3, 7, 40])
+@pytest.mark.parametrize("splits", [1, 2, 3, 7, 40, 130, 256])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_splits_with_empty_ranges(splits, dtype):
     _check(_case(6, 32, 1, 64, 700, [0, 5, 64, 129, 1, 300], dtype=dtype, seed=splits, sinks=True), num_splits=splits)
