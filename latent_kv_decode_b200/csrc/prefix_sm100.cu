@@ -246,7 +246,10 @@ __device__ __forceinline__ bool guarded(const PrefixParams& p, const TileWalk<kT
   return w.b >= 0 || w.t + kTileT > w.end || p.mask != nullptr || !ok0 || !ok1;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) prefix_sm100_kernel(const __grid_constant__ TcParams P) {
+// 96 registers: the compiler's own schedule with 121 is slower (64 sequences of 128 heads
+// behind 4096 tokens 70 us, with 104 68, with 88 to 96 64 to 66, with 80, which spills, 70;
+// which of its choices costs it is not known).
+__global__ void __maxnreg__(96) prefix_sm100_kernel(const __grid_constant__ TcParams P) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sb0 = (raw + 1023u) & ~1023u;
