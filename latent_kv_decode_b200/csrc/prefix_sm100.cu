@@ -39,8 +39,8 @@
 // busy, 1.47 PFLOP/s, where the power limit (1.42 for a long library product)
 // comes into sight. Not loading the other CTA's tokens at all (32 of 104 KB a tile)
 // gains 2%. Measured (whole call, merge included): 128 sequences of 16 heads x 2
-// queries behind 16384 tokens 164 us, 64 of 128 heads behind 4096 tokens 81 us, 4 of
-// 128 heads behind 131072 tokens 153 us: 0.90, 0.96 and 0.96 PFLOP/s, with 64, 64 and
+// queries behind 16384 tokens 156 us, 64 of 128 heads behind 4096 tokens 77 us, 4 of
+// 128 heads behind 131072 tokens 143 us: 0.95, 1.01 and 1.03 PFLOP/s, with 64, 64 and
 // 72 clusters.
 //
 // Warps (384 threads): 0 own-token producer, 1 QK issuer (CTA 0) and TMEM
