@@ -36,7 +36,7 @@
 //
 // A tile's 17 + 16 MMA steps of K = 64 take about 2870 SM cycles in the tensor
 // pipe (1.46 us); a tile takes 1.53 us in a small GPC and 1.7 with all 74 clusters
-// busy, 1.47 PFLOP/s, where the power limit (1.42 for a long library product)
+// busy, 1.49 PFLOP/s, where the power limit (1.42 for a long library product)
 // comes into sight. Not loading the other CTA's tokens at all (32 of 104 KB a tile)
 // gains 2%. Measured (whole call, merge included): 128 sequences of 16 heads x 2
 // queries behind 16384 tokens 156 us, 64 of 128 heads behind 4096 tokens 77 us, 4 of
