@@ -9,11 +9,14 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
+#include <c10/core/Event.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <limits>
+#include <memory>
 #include <string>
 #include <tuple>
 
@@ -73,22 +76,35 @@ const int32_t* int32_ptr(const OptTensor& t, const char* name, int64_t n = -1) {
   return static_cast<const int32_t*>(t->data_ptr());
 }
 
-// The device and stream of a call. The device is current while it lives; tensors
-// made for a call on another stream than the device's current one are tied to it.
+// The device and stream of a call. Both are current while it lives, so that memory
+// for the call comes from its stream's pool: a block of the caller's current stream
+// may still be in use by work queued there, which the call's stream does not wait for.
 struct Call {
   c10::cuda::CUDAGuard guard;
-  CUDAStream current, stream;
+  CUDAStream current, stream;                    // the caller's, the call's
+  std::optional<c10::cuda::CUDAStreamGuard> on;
 
   Call(const Tensor& t, OptInt handle)
       : guard(t.device()), current(c10::cuda::getCurrentCUDAStream(t.get_device())), stream(current) {
-    if (handle && reinterpret_cast<cudaStream_t>(*handle) != current.stream())
+    if (handle && reinterpret_cast<cudaStream_t>(*handle) != current.stream()) {
       stream = c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(*handle), t.get_device());
+      on.emplace(stream.unwrap());
+    }
   }
+  Call(const Call&) = delete;
+  Call& operator=(const Call&) = delete;
   void* handle() const { return stream.stream(); }
+  // The caller's tensors, which the call reads or writes on its stream.
   void used(std::initializer_list<const OptTensor*> ts) const {
     if (stream == current) return;
     for (const OptTensor* t : ts)
       if (*t) (*t)->record_stream(stream.unwrap());
+  }
+  // Tensors made here and handed out, which the caller goes on to use on its own stream.
+  void made(std::initializer_list<const OptTensor*> ts) const {
+    if (stream == current) return;
+    for (const OptTensor* t : ts)
+      if (*t) (*t)->record_stream(current.unwrap());
   }
 };
 
@@ -201,7 +217,8 @@ OptTensor rope_append(const Tensor& c_kv, const Tensor& k_pe, const Tensor& kv_c
   a.err_flag = const_cast<int32_t*>(int32_ptr(err_flag, "err_flag"));
   check_status(mla_rope_append(&a, call.handle()), "mla_rope_append");
   const OptTensor c_kv_o(c_kv);
-  call.used({&c_kv_o, &k_pe_o, &kv_o, &pe_o, &lens_o, &q_pe, &q_out, &cu_tokens, &block_table, &err_flag});
+  call.used({&c_kv_o, &k_pe_o, &kv_o, &pe_o, &lens_o, &q_pe, &q_out_given, &cu_tokens, &block_table, &err_flag});
+  if (!q_out_given) call.made({&q_out});
   return q_out;
 }
 
@@ -217,6 +234,10 @@ struct PrefixCall {
   OptTensor workspace, lse;
   Tensor x;
   std::vector<OptTensor> keep;
+  // The stream it was prepared on and its place there: what was made for the call may
+  // lie where work queued before that place is still busy. Not set while capturing.
+  std::optional<CUDAStream> home;
+  std::unique_ptr<c10::Event> ready;
 };
 
 PrefixCall prefix_make(const Tensor& q_lat, const OptTensor& q_pe, const OptTensor& prefix_kv,
@@ -317,13 +338,40 @@ PrefixCall prefix_make(const Tensor& q_lat, const OptTensor& q_pe, const OptTens
   return c;
 }
 
-std::tuple<Tensor, OptTensor> prefix_launch(PrefixCall& c, OptInt stream) {
-  Call call(c.x, stream);
+bool capturing() { return c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None; }
+
+PrefixCall prefix_prepare(const Tensor& q_lat, const OptTensor& q_pe, const OptTensor& prefix_kv,
+                          const OptTensor& prefix_pe, const OptTensor& kv_cache, const OptTensor& pe_cache,
+                          double softmax_scale, OptInt prefix_len, const OptTensor& prefix_table,
+                          const OptTensor& seq_lens, const OptTensor& block_table, int64_t page_size,
+                          const OptTensor& causal_mask, bool causal, const OptTensor& sinks, int64_t num_splits,
+                          const OptTensor& x, const OptTensor& lse, bool want_lse, const OptTensor& workspace,
+                          const OptTensor& err_flag, OptInt Lk) {
+  PrefixCall c = prefix_make(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, softmax_scale, prefix_len,
+                             prefix_table, seq_lens, block_table, page_size, causal_mask, causal, sinks, num_splits, x,
+                             lse, want_lse, workspace, err_flag, Lk);
+  const c10::cuda::CUDAGuard guard(q_lat.device());
+  c.home = c10::cuda::getCurrentCUDAStream();
+  if (!capturing()) {
+    c.ready = std::make_unique<c10::Event>(c10::DeviceType::CUDA);
+    c.ready->record(c.home->unwrap());
+  }
+  return c;
+}
+
+void prefix_enqueue(PrefixCall& c, const Call& call) {
   check_status(mla_prefix_decode(&c.a, ptr(c.workspace), c.workspace_bytes, call.handle()), "mla_prefix_decode");
+  for (const OptTensor& t : c.keep) call.used({&t});
+}
+
+std::tuple<Tensor, OptTensor> prefix_launch(PrefixCall& c, OptInt stream) {
+  const Call call(c.x, stream);
+  // a capture must not wait for work outside it; its replays are in the caller's order
+  if (c.ready && call.stream != *c.home && !capturing()) c.ready->block(call.stream.unwrap());
+  prefix_enqueue(c, call);
   const OptTensor x(c.x);
-  call.used({&x, &c.lse, &c.workspace});
-  if (!(call.stream == call.current))
-    for (const OptTensor& t : c.keep) call.used({&t});
+  for (const OptTensor* t : {&x, static_cast<const OptTensor*>(&c.lse), static_cast<const OptTensor*>(&c.workspace)})
+    if (*t && call.stream != *c.home) (*t)->record_stream(call.stream.unwrap());
   return {c.x, c.lse};
 }
 
@@ -336,17 +384,21 @@ std::tuple<Tensor, OptTensor> prefix_decode(const Tensor& q_lat, const OptTensor
                                             int64_t num_splits, const OptTensor& x, const OptTensor& lse, bool want_lse,
                                             const OptTensor& workspace, const OptTensor& err_flag, OptInt Lk,
                                             OptInt stream) {
+  need(q_lat.is_cuda(), "libmla takes CUDA tensors only");
+  const Call call(q_lat, stream);
   OptTensor mask = causal_mask;
-  if (mask && mask->is_cuda() &&
-      ((mask->scalar_type() != at::kByte && mask->scalar_type() != at::kBool) || !mask->is_contiguous())) {
-    // the copy runs on the call's stream, whose earlier work may still write the mask
-    const c10::cuda::CUDAStreamGuard on(Call(*mask, stream).stream);
-    mask = mask->ne(0).contiguous();
-  }
+  if (mask && mask->is_cuda() && mask->get_device() == q_lat.get_device() &&
+      ((mask->scalar_type() != at::kByte && mask->scalar_type() != at::kBool) || !mask->is_contiguous()))
+    mask = mask->ne(0).contiguous();   // on the call's stream, whose earlier work may still write the mask
   PrefixCall c = prefix_make(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, softmax_scale, prefix_len,
                              prefix_table, seq_lens, block_table, page_size, mask, causal, sinks, num_splits, x, lse,
                              want_lse, workspace, err_flag, Lk);
-  return prefix_launch(c, stream);
+  prefix_enqueue(c, call);
+  const OptTensor made_x(c.x);
+  call.used({&x, &lse, &workspace});
+  if (!x) call.made({&made_x});
+  if (!lse) call.made({&c.lse});
+  return {c.x, c.lse};
 }
 
 // ---------------------------------------------------------------------------
@@ -369,31 +421,27 @@ void fp4_launch(mla_fp4_linear_args& a, const Tensor& x, const Tensor& w, double
   OptTensor ws;
   if (bytes > 0) ws = at::empty({(int64_t)bytes}, x.options().dtype(at::kByte));
   check_status(mla_fp4_linear(&a, ptr(ws), bytes, call.handle()), "mla_fp4_linear");
-  const OptTensor xo(x), wo(w), oo(out);
-  call.used({&xo, &wo, &oo, &ws, &err_flag});
+  const OptTensor xo(x), wo(w);
+  call.used({&xo, &wo, &err_flag});
 }
 
 bool off16(const Tensor& t) { return reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 != 0; }
 
 // A packed copy, made on the call's stream.
-Tensor packed(const Tensor& t, const Call& call) {
-  const c10::cuda::CUDAStreamGuard on(call.stream);
-  return t.clone(at::MemoryFormat::Contiguous);
-}
+Tensor packed(const Tensor& t) { return t.clone(at::MemoryFormat::Contiguous); }
 
-Tensor fp4_linear(const Tensor& x, const Tensor& w, double scale, const OptTensor& out_given, const OptTensor& err_flag,
-                  OptInt stream) {
+Tensor linear_on(const Call& call, const Tensor& x, const Tensor& w, double scale, const OptTensor& out_given,
+                 const OptTensor& err_flag) {
   const OptTensor wo(w);
   same_device(x, {&wo, &out_given, &err_flag});
   need(x.scalar_type() == at::kBFloat16, "mla_fp4_linear takes bf16 activations");
   need(x.dim() >= 1 && w.dim() == 3 && x.size(-1) == w.size(1) * kBlock, "mla_fp4_linear: w must be (N, K/512, 288) for x (..., K)");
-  const Call call(x, stream);
   const int64_t K = x.size(-1), N = w.size(0);
   std::vector<int64_t> shape = x.sizes().vec();
   shape.back() = N;
   Tensor rows = x;
   if (x.dim() != 2 || x.stride(1) != 1 || x.stride(0) % 8 != 0 || off16(x))
-    rows = (x.is_contiguous() && !off16(x) ? x : packed(x, call)).view({-1, K});
+    rows = (x.is_contiguous() && !off16(x) ? x : packed(x)).view({-1, K});
   need(!out_given || out_given->sizes() == at::IntArrayRef(shape), "mla_fp4_linear: out has another shape");
   const Tensor out = out_given ? *out_given : at::empty(shape, x.options());
   mla_fp4_linear_args a{};
@@ -404,7 +452,15 @@ Tensor fp4_linear(const Tensor& x, const Tensor& w, double scale, const OptTenso
   a.x_batch_stride = rows.stride(0);
   a.x_block_stride = kBlock;
   fp4_launch(a, rows, w, scale, out, err_flag, call);
+  const OptTensor oo(out);
+  out_given ? call.used({&oo}) : call.made({&oo});
   return out;
+}
+
+Tensor fp4_linear(const Tensor& x, const Tensor& w, double scale, const OptTensor& out, const OptTensor& err_flag,
+                  OptInt stream) {
+  need(x.is_cuda(), "libmla takes CUDA tensors only");
+  return linear_on(Call(x, stream), x, w, scale, out, err_flag);
 }
 
 Tensor fp4_group_wo(const Tensor& x_given, const Tensor& wo_a, const OptTensor& wo_b, double scale_a, double scale_b,
@@ -416,7 +472,7 @@ Tensor fp4_group_wo(const Tensor& x_given, const Tensor& wo_a, const OptTensor& 
        "mla_fp4_group_wo: x must be (B, H, Q, 512) and wo_a (G, R, H/G, 288)");
   const Call call(x_given, stream);
   Tensor x = x_given;
-  if (x.stride(3) != 1 || x.stride(0) % 8 || x.stride(1) % 8 || x.stride(2) % 8 || off16(x)) x = packed(x, call);
+  if (x.stride(3) != 1 || x.stride(0) % 8 || x.stride(1) % 8 || x.stride(2) % 8 || off16(x)) x = packed(x);
   const int64_t B = x.size(0), Q = x.size(2), G = wo_a.size(0), R = wo_a.size(1), per = wo_a.size(2);
   const bool last = !wo_b;
   need(!last || !out || out->sizes() == at::IntArrayRef({B, Q, G * R}), "mla_fp4_group_wo: out has another shape");
@@ -432,7 +488,10 @@ Tensor fp4_group_wo(const Tensor& x_given, const Tensor& wo_a, const OptTensor& 
   a.x_group_stride = per * x.stride(1);
   a.x_block_stride = x.stride(1);
   fp4_launch(a, x, wo_a, scale_a, z, err_flag, call);
-  return last ? z : fp4_linear(z, *wo_b, scale_b, out, err_flag, stream);
+  if (!last) return linear_on(call, z, *wo_b, scale_b, out, err_flag);
+  const OptTensor zo(z);
+  out ? call.used({&zo}) : call.made({&zo});
+  return z;
 }
 
 }  // namespace
@@ -458,7 +517,7 @@ PYBIND11_MODULE(_step, m) {
       .def_readonly("x", &PrefixCall::x)
       .def_readonly("lse", &PrefixCall::lse);
   m.def("rope_append", &rope_append);
-  m.def("prefix_make", &prefix_make);
+  m.def("prefix_make", &prefix_prepare);
   m.def("prefix_launch", &prefix_launch);
   m.def("prefix_decode", &prefix_decode);
   m.def("fp4_linear", &fp4_linear);

@@ -498,7 +498,9 @@ def mla_group_wo(x, wo_a, wo_b=None, *, stream=None, **kw) -> torch.Tensor:
 # At a decode step's sizes the GPU needs these calls for a few microseconds, so
 # their marshalling is C++ (csrc/step_binding.cpp, module _step): it checks the
 # tensors, allocates outputs and workspace, and calls libmla.so on ``stream``
-# (default: the current stream of the tensors' device).
+# (default: the current stream of the tensors' device). What a call makes comes from
+# that stream's memory; the caller orders its own tensors with that stream: inputs and
+# given outputs before the call, results after it.
 
 STEP_PATH = os.path.join(_HERE, "_step.so")
 _step_mod = None
@@ -543,7 +545,7 @@ def make_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, so
                        page_size: int = 64, causal_mask=None, causal: bool = False, sinks=None,
                        num_splits: int = 0, x=None, lse=None, want_lse: bool = True, workspace=None,
                        err_flag=None, Lk: Optional[int] = None):
-    """Prepare mla_prefix_decode (no GPU work): a call with ``x``, ``lse``, ``num_splits``,
+    """Prepare mla_prefix_decode (nothing runs on the GPU): a call with ``x``, ``lse``, ``num_splits``,
     ``workspace`` and ``workspace_bytes``, to launch many times.
 
     Allocates x, lse and the workspace when not given. prefix_kv / prefix_pe:
@@ -551,6 +553,8 @@ def make_prefix_decode(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, so
     ``prefix_len``; None with ``prefix_len`` 0. kv_cache / pe_cache: the sequences'
     own tokens, laid out as for mla_decode, or None (no own tokens).
     ``causal_mask`` (uint8 or bool, contiguous) covers prefix_len + Lk positions.
+    A launch on another stream than the current one here waits, on the device, for the
+    work that is queued here now; a captured launch cannot, and its replays must follow it.
     """
     return (_step_mod or _step()).prefix_make(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, softmax_scale,
                                               prefix_len, prefix_table, seq_lens, block_table, page_size, causal_mask,
