@@ -390,6 +390,7 @@ std::tuple<Tensor, OptTensor> prefix_decode(const Tensor& q_lat, const OptTensor
   if (mask && mask->is_cuda() && mask->get_device() == q_lat.get_device() &&
       ((mask->scalar_type() != at::kByte && mask->scalar_type() != at::kBool) || !mask->is_contiguous()))
     mask = mask->ne(0).contiguous();   // on the call's stream, whose earlier work may still write the mask
+  if (mask && !mask->is_same(*causal_mask)) call.used({&causal_mask});
   PrefixCall c = prefix_make(q_lat, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cache, softmax_scale, prefix_len,
                              prefix_table, seq_lens, block_table, page_size, mask, causal, sinks, num_splits, x, lse,
                              want_lse, workspace, err_flag, Lk);
@@ -427,8 +428,12 @@ void fp4_launch(mla_fp4_linear_args& a, const Tensor& x, const Tensor& w, double
 
 bool off16(const Tensor& t) { return reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 != 0; }
 
-// A packed copy, made on the call's stream.
-Tensor packed(const Tensor& t) { return t.clone(at::MemoryFormat::Contiguous); }
+// A packed copy, made on the call's stream, which reads t.
+Tensor packed(const Tensor& t, const Call& call) {
+  const OptTensor o(t);
+  call.used({&o});
+  return t.clone(at::MemoryFormat::Contiguous);
+}
 
 Tensor linear_on(const Call& call, const Tensor& x, const Tensor& w, double scale, const OptTensor& out_given,
                  const OptTensor& err_flag) {
@@ -441,7 +446,7 @@ Tensor linear_on(const Call& call, const Tensor& x, const Tensor& w, double scal
   shape.back() = N;
   Tensor rows = x;
   if (x.dim() != 2 || x.stride(1) != 1 || x.stride(0) % 8 != 0 || off16(x))
-    rows = (x.is_contiguous() && !off16(x) ? x : packed(x)).view({-1, K});
+    rows = (x.is_contiguous() && !off16(x) ? x : packed(x, call)).view({-1, K});
   need(!out_given || out_given->sizes() == at::IntArrayRef(shape), "mla_fp4_linear: out has another shape");
   const Tensor out = out_given ? *out_given : at::empty(shape, x.options());
   mla_fp4_linear_args a{};
@@ -472,7 +477,7 @@ Tensor fp4_group_wo(const Tensor& x_given, const Tensor& wo_a, const OptTensor& 
        "mla_fp4_group_wo: x must be (B, H, Q, 512) and wo_a (G, R, H/G, 288)");
   const Call call(x_given, stream);
   Tensor x = x_given;
-  if (x.stride(3) != 1 || x.stride(0) % 8 || x.stride(1) % 8 || x.stride(2) % 8 || off16(x)) x = packed(x);
+  if (x.stride(3) != 1 || x.stride(0) % 8 || x.stride(1) % 8 || x.stride(2) % 8 || off16(x)) x = packed(x, call);
   const int64_t B = x.size(0), Q = x.size(2), G = wo_a.size(0), R = wo_a.size(1), per = wo_a.size(2);
   const bool last = !wo_b;
   need(!last || !out || out->sizes() == at::IntArrayRef({B, Q, G * R}), "mla_fp4_group_wo: out has another shape");

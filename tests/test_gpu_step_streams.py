@@ -108,3 +108,45 @@ def test_a_prepared_call_in_a_capture():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(c.x, want[0]) and torch.equal(c.lse, want[1])
+
+
+def _odd(t):
+    """The same values in rows that no call reads in place: packed, but two bytes off the wide accesses."""
+    wide = torch.zeros((*t.shape[:-1], t.shape[-1] + 3), dtype=t.dtype, device=t.device)
+    wide[..., 3:] = t
+    return wide[..., 3:]
+
+
+@pytest.mark.parametrize("name", ["product", "product in blocks", "groups", "chain", "float mask", "strided mask"])
+def test_inputs_that_are_copied_and_dropped_while_the_copy_waits(name):
+    # the call's stream has not reached the copy when the caller drops the input and
+    # asks for its memory again
+    from latent_kv_decode_b200 import ops
+    d = _inputs()
+    g = torch.Generator("cuda").manual_seed(43)
+    seen = torch.rand(700, generator=g, device="cuda") < 0.5
+    prefix = lambda m, **kw: ops.mla_prefix_decode(d["q_lat"], d["q_pe"], d["rows"][:, :C], d["rows"][:, C:], None, None,
+                                                   0.07, causal_mask=m, **kw)
+    make, call = {
+        "product": (lambda: _odd(d["x"]), lambda x, **kw: ops.mla_fp4_linear(x, d["w"], 0.01, **kw)),
+        "product in blocks": (lambda: _odd(d["x"].view(4, 10, 2048)), lambda x, **kw: ops.mla_fp4_linear(x, d["w"], 0.01, **kw)),
+        "groups": (lambda: _odd(d["x4"]), lambda x, **kw: ops.mla_fp4_group_wo(x, d["wa"], scale_a=0.01, **kw)),
+        "chain": (lambda: _odd(d["x4"]), lambda x, **kw: ops.mla_fp4_group_wo(x, d["wa"], d["wb"], scale_a=0.01, scale_b=0.01, **kw)),
+        "float mask": (lambda: seen.float(), prefix),
+        "strided mask": (lambda: torch.stack([seen, seen], 1)[:, 0], prefix),
+    }[name]
+    out = lambda r: r if isinstance(r, tuple) else (r,)
+    want = [t.clone() for t in out(call(make()))]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a = make()
+    size = a.untyped_storage().nbytes()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(SLEEP)
+    got = out(call(a, stream=s))
+    del a
+    junk = [torch.full((size,), 0x31, dtype=torch.uint8, device="cuda") for _ in range(4)]     # where it was
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del junk
