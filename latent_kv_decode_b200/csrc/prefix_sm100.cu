@@ -229,8 +229,9 @@ __device__ __forceinline__ bool bad_pages(const PrefixParams& p, const int* lens
   bool bad = false;
   const int64_t ps = p.page_size;
   if (p.ptable) {
-    const int end = min(p.Lp, (j0 + nt) * kTileT);
-    for (int64_t i = j0 * kTileT / ps + tid; i * ps < end; i += n) bad = bad || p.ptable[i] < 0 || p.ptable[i] >= p.p_pages;
+    // 64 bits: a block's tiles, up to 17 sequences', may hold more than 2^31 tokens
+    const int64_t first = (int64_t)j0 * kTileT, end = min((int64_t)p.Lp, first + (int64_t)nt * kTileT);
+    for (int64_t i = first / ps + tid; i * ps < end; i += n) bad = bad || p.ptable[i] < 0 || p.ptable[i] >= p.p_pages;
   }
   if (p.table)
     for (int b = b0; b <= b1; ++b) {

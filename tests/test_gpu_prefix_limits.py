@@ -1,0 +1,52 @@
+"""mla_prefix_decode at the ends of its range, against the formula in 64 bits: token
+counts beyond 32 bits, long prefixes, sinks of -inf, rows that reach back into the
+prefix, references that move.
+"""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+C, DR = 512, 64
+HALF = torch.finfo(torch.bfloat16).eps / 2     # of a rounding to bf16
+
+
+def _attend(q, k, scale, sink=None):
+    """Rows of q (n, C + DR) over the tokens k (t, C + DR), both float64: x, lse, sum_t p_t |v_t|."""
+    s = q @ k.T * scale
+    if sink is not None:
+        s = torch.cat([s, sink[:, None]], 1)
+        k = torch.cat([k, torch.zeros_like(k[:1])])
+    lse = torch.logsumexp(s, -1)
+    p = torch.exp(s - lse[:, None])
+    return p @ k[:, :C], lse, p @ k[:, :C].abs()
+
+
+def test_a_block_of_more_than_2_to_the_31_tokens():
+    # sixteen sequences of one block, 2^27 + 2^22 own tokens each, all in one page that their
+    # tables repeat; the mask leaves the prefix's first 100 tokens and the last 200
+    from latent_kv_decode_b200 import ops
+    B, H, page, Lp, n = 16, 8, 4096, 128, 2 ** 27 + 2 ** 22
+    g = torch.Generator("cuda").manual_seed(51)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    pool, q = r(2, page, C + DR), r(B, H, 1, C + DR) * 0.8
+    mask = torch.zeros(Lp + n, dtype=torch.uint8, device="cuda")
+    mask[:100] = 1
+    mask[-200:] = 1
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x, lse = ops.mla_prefix_decode(q[..., :C].contiguous(), q[..., C:].contiguous(), pool[..., :C], pool[..., C:],
+                                   pool[..., :C], pool[..., C:], 0.07, prefix_len=Lp,
+                                   prefix_table=torch.zeros(1, dtype=torch.int32, device="cuda"), page_size=page,
+                                   block_table=torch.ones((B, n // page), dtype=torch.int32, device="cuda"),
+                                   causal_mask=mask, err_flag=err)
+    assert int(err.item()) == 0
+    k = torch.cat([pool[0, :100], pool[1, -200:]]).double()
+    want, want_lse, size = _attend(q.double().reshape(B * H, -1), k, 0.07)
+    # a weight and x are rounded once to bf16; 300 float32 additions of either sum
+    tol = HALF * (size + want.abs()) + 300 * 2.0 ** -23 * size
+    assert ((x.double().reshape(B * H, C) - want).abs() <= tol).all()
+    # scores are float32 sums of 576 products
+    at = 576 * 2.0 ** -24 * (q.double().abs().reshape(B * H, -1) @ k.abs().T).amax(1) * 0.07 + 300 * 2.0 ** -24
+    assert ((lse.double().reshape(-1) - want_lse).abs() <= at).all()
