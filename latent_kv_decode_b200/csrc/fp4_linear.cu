@@ -476,6 +476,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_linear_kernel(const __grid_co
         if (n + k < P.N) out[k] = __float2bfloat16_rn(y[k]);
     }
   }
+  if (failed) {                              // a wait gave up: no copy or MMA may outlive the block
+    const uint64_t begin = global_ns();
+    while (global_ns() - begin < 50000ull) {
+    }
+  }
   cluster_sync();                            // the peers have read this CTA's sums
   if (warp == kConv / 32 + 1) tmem_dealloc(tmem, kTmemCols);
 }

@@ -309,7 +309,8 @@ __global__ void __maxnreg__(96) prefix_sm100_kernel(const __grid_constant__ TcPa
     *abort_flag = 1;
     prefix_flag(p, MLA_DEVICE_ERR_TIMEOUT);
   };
-  // let copies already issued land before this CTA's shared memory goes away
+  // after a timeout: let copies and MMAs already issued end before this CTA's shared
+  // memory and tensor memory go away
   auto settle = []() {
     const uint64_t t0 = global_ns();
     while (global_ns() - t0 < 50000ull) {
@@ -341,10 +342,7 @@ __global__ void __maxnreg__(96) prefix_sm100_kernel(const __grid_constant__ TcPa
         if (*abort_flag) ok = false;
         w.next(lens, b0);
       }
-      if (!ok) {
-        fail();
-        settle();
-      }
+      if (!ok) fail();
     }
     __syncwarp();
   } else if (warp == 2) {
@@ -406,10 +404,7 @@ __global__ void __maxnreg__(96) prefix_sm100_kernel(const __grid_constant__ TcPa
       ok = __all_sync(0xffffffffu, ok);
       w.next(lens, b0);
     }
-    if (!ok && lane == 0) {
-      fail();
-      settle();
-    }
+    if (!ok && lane == 0) fail();
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ QK issuer (CTA 0)
@@ -794,6 +789,7 @@ __global__ void __maxnreg__(96) prefix_sm100_kernel(const __grid_constant__ TcPa
   if (ntiles == 0 && rank == 0 && threadIdx.x == 0 && !mbar_wait_cluster(bar(B_QFULL), 0)) fail();
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag) settle();                  // whichever wait gave up: no copy or MMA outlives the block
   cluster_sync();
   if (warp == 1) {
     tc_fence_after();
