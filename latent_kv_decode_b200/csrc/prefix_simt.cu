@@ -438,8 +438,10 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
       float wt = 1.f;
       if (!parts && p.sinks) {
         const float sk = p.sinks[(r % p.HQ) / p.Q], m2 = fmaxf(m, sk);
-        wt = m == -INFINITY ? 0.f : expf(m - m2);
-        l = l * wt + expf(sk - m2);
+        if (m2 != -INFINITY) {                   // else nothing was seen and the sink adds nothing
+          wt = m == -INFINITY ? 0.f : expf(m - m2);
+          l = l * wt + expf(sk - m2);
+        }
         m = m2;
       }
       const bool seen = !(m == -INFINITY && l == 0.f);   // a NaN denominator stays one

@@ -50,3 +50,28 @@ def test_a_block_of_more_than_2_to_the_31_tokens():
     # scores are float32 sums of 576 products
     at = 576 * 2.0 ** -24 * (q.double().abs().reshape(B * H, -1) @ k.abs().T).amax(1) * 0.07 + 300 * 2.0 ** -24
     assert ((lse.double().reshape(-1) - want_lse).abs() <= at).all()
+
+
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sinks_of_minus_infinity(dtype, splits):
+    # such a sink adds nothing: rows that see nothing give x = 0 and lse = -inf, the others
+    # what they give without it
+    from latent_kv_decode_b200 import ops
+    B, H = 3, 16
+    g = torch.Generator("cuda").manual_seed(52)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(dtype)
+    q_lat, q_pe, own = r(B, H, 1, C), r(B, H, 1, DR), r(B, 70, C + DR)
+    lens = torch.tensor([0, 70, 1], dtype=torch.int32, device="cuda")
+    call = lambda sinks: ops.mla_prefix_decode(q_lat, q_pe, None, None, own[..., :C], own[..., C:], 0.07, seq_lens=lens,
+                                               sinks=sinks, num_splits=splits)
+    bare = call(None)
+    off = call(torch.full((H,), -math.inf, device="cuda"))
+    half = torch.randn(H, generator=g, device="cuda")
+    some = call(half)
+    half[::2] = -math.inf
+    both = call(half)
+    assert (bare[0][0] == 0).all() and (bare[1][0] == -math.inf).all()
+    for got, want in ((off, bare), ([t[:, ::2] for t in both], [t[:, ::2] for t in bare]),
+                      ([t[:, 1::2] for t in both], [t[:, 1::2] for t in some])):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
