@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
       for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       const float m_new = fmaxf(m_run[i], mx);
       const float al = m_run[i] == -INFINITY ? 0.f : expf(m_run[i] - m_new);
-      const float e = vis ? expf(s - m_new) : 0.f;
+      const float e = s != -INFINITY ? expf(s - m_new) : 0.f;   // also a visible score of -inf, whatever m_new
       float sum = e;
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);

@@ -75,3 +75,43 @@ def test_sinks_of_minus_infinity(dtype, splits):
     for got, want in ((off, bare), ([t[:, ::2] for t in both], [t[:, ::2] for t in bare]),
                       ([t[:, 1::2] for t in both], [t[:, 1::2] for t in some])):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("splits", [1, 2])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_first_score_of_minus_infinity(dtype, splits, page):
+    # the prefix's one token has +inf in a position channel: rows with a negative query there
+    # give it the weight e^-inf = 0 and go on, rows with a positive one are NaN
+    from latent_kv_decode_b200 import ops
+    B, H, n = 3, 16, 40
+    g = torch.Generator("cuda").manual_seed(53)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(dtype)
+    q, own, first = r(B, H, 1, C + DR), r(B, n, C + DR), r(1, C + DR)
+    first[0, C + 5] = math.inf
+    kw = dict(num_splits=splits)
+    if page:
+        per = -(-n // page)
+        pool = torch.zeros((B * per + 1, page, C + DR), dtype=dtype, device="cuda")
+        pool[0, 0] = first[0]
+        pool[1:].view(B, per * page, -1)[:, :n] = own
+        table = torch.arange(1, B * per + 1, dtype=torch.int32, device="cuda").view(B, per)
+        kw.update(prefix_len=1, prefix_table=torch.zeros(1, dtype=torch.int32, device="cuda"), block_table=table,
+                  page_size=page, seq_lens=torch.full((B,), n, dtype=torch.int32, device="cuda"))
+        prefix = own_rows = pool
+    else:
+        prefix, own_rows = first, own
+    x, lse = ops.mla_prefix_decode(q[..., :C].contiguous(), q[..., C:].contiguous(), prefix[..., :C], prefix[..., C:],
+                                   own_rows[..., :C], own_rows[..., C:], 0.07, **kw)
+    lost = q[:, :, 0, C + 5] > 0
+    assert lost.any() and not lost.all()
+    assert torch.isnan(x[:, :, 0][lost]).all() and torch.isnan(lse[..., 0][lost]).all()
+    for b in range(B):
+        k = own[b].double()
+        want, want_lse, size = _attend(q[b, :, 0].double(), k, 0.07)
+        # float32 sums of 576 products shift a weight by e^at; bf16 rounds weights and x once more
+        at = 2 * 576 * 2.0 ** -24 * (q[b, :, 0].double().abs() @ k.abs().T).amax(1) * 0.07 + n * 2.0 ** -23
+        tol = at[:, None] * size + (HALF * (size + want.abs()) if dtype == torch.bfloat16 else 0)
+        keep = ~lost[b]
+        assert ((x[b, :, 0].double() - want).abs() <= tol)[keep].all()
+        assert ((lse[b, :, 0].double() - want_lse).abs() <= at)[keep].all()
