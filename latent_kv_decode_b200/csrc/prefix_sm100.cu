@@ -30,7 +30,7 @@
 //
 // A weight of 0 does not silence an infinity or NaN in V. Tiles that may hold
 // rows which some query must not see ("guarded": own tokens, a tile's ragged
-// end, a mask, a bad page) are cleaned before the aggregation: warp 2 zeroes
+// end, the prefix's end behind a causal row's last token, a mask, a bad page) are cleaned before the aggregation: warp 2 zeroes
 // the rows no query may see, and if S shows a non-finite key, the softmax warps
 // zero the non-finite values (the rows that see that key are NaN by their S).
 //
@@ -242,9 +242,16 @@ __device__ __forceinline__ bool bad_pages(const PrefixParams& p, const int* lens
   return bad;
 }
 
+// The prefix tokens that every row of the block is sure to see. With fewer own tokens
+// than queries, a causal row ends before the prefix does. For a whole warp.
+__device__ __forceinline__ int seen_by_all(const PrefixParams& p, const int* lens, int b0, int b1, int lane) {
+  const int least = __reduce_min_sync(0xffffffffu, lane <= b1 - b0 ? lens[lane] : 0x7fffffff);
+  return p.mask ? 0 : p.causal ? p.Lp + min(0, least - p.Q + 1) : p.Lp;
+}
+
 // May the tile hold rows that some query must not see?
-__device__ __forceinline__ bool guarded(const PrefixParams& p, const TileWalk<kTileT>& w, bool ok0, bool ok1) {
-  return w.b >= 0 || w.t + kTileT > w.end || p.mask != nullptr || !ok0 || !ok1;
+__device__ __forceinline__ bool guarded(const TileWalk<kTileT>& w, int to_all, bool ok0, bool ok1) {
+  return w.b >= 0 || w.t + kTileT > to_all || !ok0 || !ok1;
 }
 
 // 96 registers: the compiler's own schedule with 121 is slower (64 sequences of 128 heads
@@ -356,11 +363,12 @@ __global__ void __maxnreg__(96) prefix_sm100_kernel(const __grid_constant__ TcPa
     bool ok = true;
     int ng = 0;
     const bool look = __any_sync(0xffffffffu, bad_pages(p, lens, b0, b1, j_begin, ntiles, lane, 32));
+    const int to_all = seen_by_all(p, lens, b0, b1, lane);
     for (int j = 0; j < ntiles && ok; ++j) {
       const int s = j & 1;
       const Block64 peer = block64(p, w, 1 - (int)rank);
       const bool own_ok = !look || block64(p, w, (int)rank).ok;
-      const bool g = guarded(p, w, own_ok, peer.ok);
+      const bool g = guarded(w, to_all, own_ok, peer.ok);
       if (lane == 0) {
         ok = mbar_wait_cluster(bar((rank == 0 ? B_SFULL : B_QH0) + s), (j >> 1) & 1);
         if (ok) {
@@ -526,6 +534,7 @@ __global__ void __maxnreg__(96) prefix_sm100_kernel(const __grid_constant__ TcPa
     const int last_pos = !live ? -1 : p.causal ? p.Lp + lens[my_b - b0] - p.Q + r % p.Q : 0x3fffffff;
 
     const bool look = bar_or(1, kSoft, bad_pages(p, lens, b0, b1, j_begin, ntiles, xi, kSoft));
+    const int to_all = seen_by_all(p, lens, b0, b1, lane);
 
     for (int j = 0; j < ntiles; ++j) {
       const int sb = j & 1;
@@ -536,7 +545,7 @@ __global__ void __maxnreg__(96) prefix_sm100_kernel(const __grid_constant__ TcPa
         ok0 = block64(p, w, 0).ok;
         ok1 = block64(p, w, 1).ok;
       }
-      const bool gd = guarded(p, w, ok0, ok1);
+      const bool gd = guarded(w, to_all, ok0, ok1);
       int lim = min(w.end, last_pos - base + 1) - ts;          // tokens [ts, ts + lim) pass all but the mask
       if (!live || (w.b >= 0 && w.b != my_b) || !(half ? ok1 : ok0)) lim = 0;
       uint32_t vis = kAll;                                     // the mask over [ts, ts + kTok), the same across the warp

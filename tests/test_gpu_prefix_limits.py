@@ -115,3 +115,50 @@ def test_a_first_score_of_minus_infinity(dtype, splits, page):
         keep = ~lost[b]
         assert ((x[b, :, 0].double() - want).abs() <= tol)[keep].all()
         assert ((lse[b, :, 0].double() - want_lse).abs() <= at)[keep].all()
+
+
+@pytest.mark.parametrize("Lp,lens", [(128, [0, 1, 2, 3]), (256, [3, 0, 4, 9]), (256, [2, 4, 9, 200])])
+@pytest.mark.parametrize("page", [0, 64])
+@pytest.mark.parametrize("splits", [1, 2])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_bad_last_prefix_row_stays_hidden_from_causal_rows(dtype, bad, splits, page, Lp, lens):
+    # fewer own tokens than queries: the first queries do not see the prefix's last row, which
+    # ends a full tile and holds NaN or infinity in its latent part; the rows that see it are NaN
+    from latent_kv_decode_b200 import ops
+    B, H, Q = len(lens), 8, 4
+    g = torch.Generator("cuda").manual_seed(54)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(dtype)
+    q, own, prefix = r(B, H, Q, C + DR), r(B, max(lens), C + DR), r(Lp, C + DR)
+    prefix[-1, 7] = bad
+    kw = dict(seq_lens=torch.tensor(lens, dtype=torch.int32, device="cuda"), causal=True, num_splits=splits)
+    a, b = prefix, own
+    if page:
+        n = Lp // page
+        per = -(-max(lens) // page)
+        pool = torch.zeros((n + B * per, page, C + DR), dtype=dtype, device="cuda")
+        pool[:n] = prefix.view(n, page, -1)
+        pool[n:].view(B, per * page, -1)[:, :max(lens)] = own
+        i32 = lambda t: t.to(torch.int32).cuda()
+        kw.update(prefix_len=Lp, prefix_table=i32(torch.arange(n)), page_size=page,
+                  block_table=i32(torch.arange(n, n + B * per).view(B, per)))
+        a = b = pool
+    x, lse = ops.mla_prefix_decode(q[..., :C].contiguous(), q[..., C:].contiguous(), a[..., :C], a[..., C:], b[..., :C],
+                                   b[..., C:], 0.07, **kw)
+    hidden = 0
+    for s in range(B):
+        k = torch.cat([prefix, own[s, :lens[s]]]).double()
+        for i in range(Q):
+            n = Lp + lens[s] - Q + i + 1
+            qq = q[s, :, i].double()
+            if n >= Lp:
+                seen = q[s, :, i, 7] > 0 if bad == math.inf else torch.ones(H, dtype=torch.bool, device="cuda")
+                assert torch.isnan(x[s, :, i][seen]).all() and torch.isnan(lse[s, :, i][seen]).all()
+                continue
+            hidden += 1
+            want, want_lse, size = _attend(qq, k[:n], 0.07)
+            at = 2 * 576 * 2.0 ** -24 * (qq.abs() @ k[:n].abs().T).amax(1) * 0.07 + n * 2.0 ** -23
+            tol = at[:, None] * size + (HALF * (size + want.abs()) if dtype == torch.bfloat16 else 0)
+            assert ((x[s, :, i].double() - want).abs() <= tol).all()
+            assert ((lse[s, :, i].double() - want_lse).abs() <= at).all()
+    assert hidden > 0
