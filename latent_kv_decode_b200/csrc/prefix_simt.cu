@@ -9,13 +9,18 @@
 //                  a time, a lane per token.
 //   O += P . V     a warp owns 64 of the 512 columns.
 // The products are mma.m16n8k16 on bf16 parts: a float32 value is the sum of three
-// bf16, exactly (down to their smallest, 2^-133), and of the nine products of two such sums the six largest count
-// (the others are below 2^-25 of the first), added in float32. Q is split once per
-// CTA, K and V as their fragments are read, the weights by the softmax. Measured: 4.1
-// us a tile (S 1.5, softmax 0.8, O 1.1), where packed float32 FMAs, which shared
-// memory feeds with 32 floats a clock, took 5.4; 128 rows behind 2049 tokens 39 -> 31
-// us. (The warp-level instruction, as its operands come from registers, split there;
-// for tcgen05 the parts would have to be written to shared memory in its layout.)
+// bf16, exactly (down to their smallest, 2^-133), and of the nine products of two such
+// sums the six largest count (the others are below 2^-25 of the first). With bf16 inputs
+// a score is one product, and a weight, a float32, two parts (to 2^-18 of it). The
+// instruction adds in float32 and truncates, so what it adds up is kept short: a warp's
+// part of a score is at most 30 such additions, a tile's share of O six; parts and
+// tiles are added by rounding instructions. Behind 131072 tokens in one range x is
+// then within 7e-6 where O in the instruction's accumulator had lost 1e-3 of it. Q is
+// split once per CTA, K and V as their fragments are read, the weights by the softmax.
+// Measured: 4.1 us a tile (S 1.5, softmax 0.8, O 1.1), where packed float32 FMAs, which
+// shared memory feeds with 32 floats a clock, took 5.4; 128 rows behind 2049 tokens 39
+// -> 31 us. (The warp-level instruction, as its operands come from registers, split
+// there; for tcgen05 the parts would have to be written to shared memory in its layout.)
 //
 // Tokens that no row may see are zeros in the tile, so whatever their cache
 // rows hold stays out of the sums; where a tile that some rows do not see holds
@@ -123,8 +128,7 @@ __device__ __forceinline__ void load_rows(float* dst, int D, Lat lat, Pe pe) {
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
+template <typename T> __device__ __forceinline__ void decode_range(const PrefixParams& p) {
   extern __shared__ float smem[];
   __shared__ const T* row_lat[2][kToks];         // the tile's cache rows, null where no row may see the token
   __shared__ const T* row_pe[2][kToks];
@@ -359,16 +363,11 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
       if (tok == 0) alpha[srow] = al;
     }
     __syncthreads();
+    float al[2][2];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      const float al0 = alpha[16 * m + gid], al1 = alpha[16 * m + 8 + gid];
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        acc[m][n][0] *= al0;
-        acc[m][n][1] *= al0;
-        acc[m][n][2] *= al1;
-        acc[m][n][3] *= al1;
-      }
+      al[m][0] = alpha[16 * m + gid];
+      al[m][1] = alpha[16 * m + 8 + gid];
     }
     const float* vt = kt + 64 * warp;
     if (!any_odd) {
@@ -389,16 +388,27 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
         uint32_t v0[kP], v1[kP];
         split<kP>(v[0], v[4 * pitch], v0);
         split<kP>(v[8 * pitch], v[12 * pitch], v1);
+        float c[2][4] = {};                      // the tile's own sum
 #pragma unroll
         for (int sum = kWP - 1; sum >= 0; --sum)
 #pragma unroll
           for (int i = 0; i < kP; ++i)
             if (sum - i >= 0)
 #pragma unroll
-              for (int m = 0; m < 2; ++m) mma16816(acc[m][n], pa[m][sum - i], v0[i], v1[i]);
+              for (int m = 0; m < 2; ++m) mma16816(c[m], pa[m][sum - i], v0[i], v1[i]);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[m][n][k] = fmaf(acc[m][n][k], al[m][k >> 1], c[m][k]);
       }
     } else {
       // rows whose weight is 0 skip the token
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[m][n][k] *= al[m][k >> 1];
 #pragma unroll 1
       for (int t = 0; t < kToks; ++t) {
         const int pos = ((t >> 3) << 3) + 2 * (t & 3) + ((t >> 2) & 1);
@@ -477,6 +487,17 @@ __global__ void __launch_bounds__(kThr) prefix_simt(const PrefixParams p) {
           *reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(p.x) + (int64_t)r * p.Ckv + c) = sm100::pack_bf16(v.x, v.y);
       }
     }
+}
+
+// One CTA fills an SM. The compiler's own choice of registers is 168 for float32, which leaves
+// room for the merge to start early (8 x 16 heads behind 2049 tokens 31.2 us, with 241 registers
+// 32.0, where 64 x 16 behind 4096 take 305 and 291); for bf16 it is 128 and spills (245 : 209 us).
+template <typename T> __global__ void prefix_simt(const __grid_constant__ PrefixParams p);
+template <> __global__ void __launch_bounds__(kThr) prefix_simt<float>(const __grid_constant__ PrefixParams p) {
+  decode_range<float>(p);
+}
+template <> __global__ void __launch_bounds__(kThr, 1) prefix_simt<__nv_bfloat16>(const __grid_constant__ PrefixParams p) {
+  decode_range<__nv_bfloat16>(p);
 }
 
 template <typename T>

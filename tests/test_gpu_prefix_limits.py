@@ -162,3 +162,67 @@ def test_a_bad_last_prefix_row_stays_hidden_from_causal_rows(dtype, bad, splits,
             assert ((x[s, :, i].double() - want).abs() <= tol).all()
             assert ((lse[s, :, i].double() - want_lse).abs() <= at).all()
     assert hidden > 0
+
+
+@pytest.mark.parametrize("page", [0, 16])
+def test_float32_over_a_long_prefix_in_one_range(page):
+    # Values of nonzero mean, so that O grows with every one of the 8192 tiles of 16 tokens.
+    # Rounded sums: errors of either sign, of which n are within 7 sqrt(n) 2^-24 but for one in
+    # 10^10 (Higham and Mary, 2019), for O and for the denominator; a tile's own products, a
+    # few truncations of 2^-23 each; the scores, sums of 576 products, are small here.
+    from latent_kv_decode_b200 import ops
+    H, Lp = 8, 131072
+    g = torch.Generator("cuda").manual_seed(55)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")
+    q, rows = r(1, H, 1, C + DR) * 0.01, r(Lp, C + DR) * 0.5 + 1.0
+    kw = dict(num_splits=1)
+    k = rows
+    if page:
+        perm = torch.randperm(Lp // page, generator=torch.Generator().manual_seed(5)).cuda()
+        pool = torch.empty((Lp // page, page, C + DR), device="cuda")
+        pool[perm] = rows.view(-1, page, C + DR)
+        kw.update(prefix_len=Lp, prefix_table=perm.to(torch.int32), page_size=page)
+        rows = pool
+    x, lse = ops.mla_prefix_decode(q[..., :C].contiguous(), q[..., C:].contiguous(), rows[..., :C], rows[..., C:], None,
+                                   None, 0.07, **kw)
+    qq, k = q[0, :, 0].double(), k.double()
+    want, want_lse, size = _attend(qq, k, 0.07)
+    at = 576 * 2.0 ** -24 * (qq.abs() @ k.abs().T).amax(1) * 0.07
+    sums = 7 * math.sqrt(Lp / 16) * 2.0 ** -24
+    tol = (2 * sums + 16 * 2.0 ** -23 + 2 * at)[:, None] * size
+    err = (x[0, :, 0].double() - want).abs()
+    assert (err <= tol).all(), f"{(err / size).max().item():.2e} of the values"
+    assert ((lse[0, :, 0].double() - want_lse).abs() <= at + sums + 2.0 ** -23 * want_lse.abs()).all()
+
+
+@pytest.mark.parametrize("splits", [0, 1, 5])
+@pytest.mark.parametrize("Lp,B,H,Q,lens", [(131072, 1, 128, 1, [130]), (16384, 16, 16, 2, [2, 40, 129, 511] * 4),
+                                           (4097, 2, 128, 1, [1, 500])])
+def test_bf16_over_long_prefixes(Lp, B, H, Q, lens, splits):
+    # the sizes the call is made for, paged, every row against 64 bits. A weight and x are
+    # rounded once to bf16; O is a sum of one addition per 16 tokens (at most 2^-23 each, a
+    # truncation), the denominator one per tile and thread
+    from latent_kv_decode_b200 import ops
+    g = torch.Generator("cuda").manual_seed(56)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    page, n, per = 64, -(-Lp // 64), -(-max(lens) // 64)
+    perm = torch.randperm(n + B * per, generator=torch.Generator().manual_seed(6)).to(torch.int32).cuda()
+    pool, q = r(n + B * per, page, C + DR), r(B, H, Q, C + DR) * 0.8
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x, lse = ops.mla_prefix_decode(q[..., :C].contiguous(), q[..., C:].contiguous(), pool[..., :C], pool[..., C:],
+                                   pool[..., :C], pool[..., C:], 0.07, prefix_len=Lp, prefix_table=perm[:n],
+                                   block_table=perm[n:].view(B, per).contiguous(), causal=True, num_splits=splits,
+                                   seq_lens=torch.tensor(lens, dtype=torch.int32, device="cuda"), err_flag=err)
+    assert int(err.item()) == 0
+    flat = lambda ids, m: pool[ids.long()].flatten(0, 1)[:m].double()
+    prefix = flat(perm[:n], Lp)
+    for b in range(B):
+        k = torch.cat([prefix, flat(perm[n:].view(B, per)[b], lens[b])])
+        for i in range(Q):
+            seen = Lp + lens[b] - Q + i + 1
+            qq = q[b, :, i].double()
+            want, want_lse, size = _attend(qq, k[:seen], 0.07)
+            at = 576 * 2.0 ** -24 * (qq.abs() @ k.abs().T).amax(1) * 0.07
+            tol = HALF * (size + want.abs()) + ((seen / 16) * 2.0 ** -23 + 2 * at[:, None]) * size
+            assert ((x[b, :, i].double() - want).abs() <= tol).all()
+            assert ((lse[b, :, i].double() - want_lse).abs() <= at + seen / 128 * 2.0 ** -24 + 2.0 ** -22 * want_lse.abs()).all()
