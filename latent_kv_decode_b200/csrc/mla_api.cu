@@ -464,7 +464,7 @@ mla_status_t validate_prefix(const mla_prefix_args* a) {
   // stacked rows (times splits) and positions are 32-bit
   if ((int64_t)a->B * a->H * a->Q > (1 << 24) || (int64_t)a->prefix_len + a->Lk > (1 << 30))
     return MLA_ERR_UNSUPPORTED;
-  if (a->num_splits < 0 || a->num_splits > kMaxSplits) return MLA_ERR_INVALID_ARG;
+  if (a->num_splits < 0 || a->num_splits > mla::kPrefixMaxSplits) return MLA_ERR_INVALID_ARG;
   if (!a->q_lat || !a->x || (a->Dr > 0 && !a->q_pe)) return MLA_ERR_INVALID_ARG;
   if (a->prefix_len > 0 && (!a->prefix_kv || (a->Dr > 0 && !a->prefix_pe))) return MLA_ERR_INVALID_ARG;
   if (a->Lk > 0 && (!a->kv_cache || (a->Dr > 0 && !a->pe_cache))) return MLA_ERR_INVALID_ARG;

@@ -98,6 +98,8 @@ struct TileWalk {
   }
 };
 
+constexpr int kPrefixMaxSplits = 256;   // ranges of a block that the merge holds the weights of
+
 // At most s ranges (1 if less), as few as keep the longest as short: ranges that
 // would be empty or shorter only lengthen the merge.
 inline int even_splits(int64_t tiles, int64_t s) {

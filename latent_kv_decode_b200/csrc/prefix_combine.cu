@@ -20,7 +20,7 @@ __global__ void __launch_bounds__(kQuarters* kShare > 1 ? 32 * kQuarters * kShar
     prefix_combine(const PrefixParams p) {
   constexpr bool kRowPerCta = kQuarters * kShare > 1;
   constexpr int kCols = kCkv / 32 / kQuarters, kGroup = kRowPerCta ? 8 : 4;
-  constexpr int kHeld = 8;                       // weights a lane keeps: 256 splits, the most a call takes
+  constexpr int kHeld = kPrefixMaxSplits / 32;   // weights a lane keeps
   __shared__ float4 sums[kShare > 1 ? kShare - 1 : 1][kCkv / 4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t r = kRowPerCta ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + warp;

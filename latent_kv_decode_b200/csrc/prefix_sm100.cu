@@ -865,15 +865,20 @@ bool prefix_sm100_supported(const mla_prefix_args* a) {
          }) == cudaSuccess;
 }
 
-// As many clusters as run at once, but no range shorter than a tile of the blocks'
-// most: down to one tile a range the merge costs less than the tiles it spares (16
-// sequences of 8 heads, 500 + 100 tokens: 43, 22, 16 us with 1, 5, 20 ranges).
+// As many clusters as run at once, but no range shorter than a tile of the blocks' most
+// (own tokens counted as the storage allows, their lengths being on the device): down to
+// one tile a range the merge costs less than the tiles it spares (16 sequences of 8
+// heads, 500 + 100 tokens: 43, 22, 16 us with 1, 5, 20 ranges). And no range much above
+// 2^18 tokens: the tensor pipe adds to O once per 16 tokens and truncates, which takes
+// more of x the longer the range (behind 2^17, 2^20, 2^22 tokens of equal weight 0.0008,
+// 0.006 and 0.024 of it, where a rounding to bf16 takes at most 0.0039).
 int prefix_sm100_auto_splits(const mla_prefix_args* a, int sms) {
   const int pairs = sms / 2, HQ = a->H * a->Q;
   const int64_t blocks = ((int64_t)a->B * HQ + kRowsT - 1) / kRowsT;
   const int64_t seqs = std::min<int64_t>(a->B, (kRowsT + HQ - 1) / HQ);   // of a block
   const int64_t tiles = ((int64_t)a->prefix_len + kTileT - 1) / kTileT + seqs * ((a->Lk + kTileT - 1) / kTileT);
-  return even_splits(tiles, std::min(pairs / blocks, tiles));
+  const int64_t least = std::min<int64_t>(((int64_t)a->prefix_len + a->Lk + (1 << 18) - 1) >> 18, kPrefixMaxSplits);
+  return even_splits(tiles, std::max(std::min(pairs / blocks, tiles), least));
 }
 
 cudaError_t launch_prefix_sm100(const PrefixParams& p, cudaStream_t st) {

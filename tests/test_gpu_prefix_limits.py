@@ -226,3 +226,26 @@ def test_bf16_over_long_prefixes(Lp, B, H, Q, lens, splits):
             tol = HALF * (size + want.abs()) + ((seen / 16) * 2.0 ** -23 + 2 * at[:, None]) * size
             assert ((x[b, :, i].double() - want).abs() <= tol).all()
             assert ((lse[b, :, i].double() - want_lse).abs() <= at + seen / 128 * 2.0 ** -24 + 2.0 ** -22 * want_lse.abs()).all()
+
+
+@pytest.mark.parametrize("H,B", [(128, 40), (16, 300)])
+def test_bf16_sums_over_two_million_tokens(H, B):
+    # more blocks of rows than clusters, so that speed alone asks for one range; values of
+    # nonzero mean. A weight and x are rounded once to bf16, and O is a sum of at most 2^14
+    # additions a range (one per 16 tokens, a truncation of at most 2^-23), merged by rounding ones
+    from latent_kv_decode_b200 import ops
+    n, pages, page = 2 ** 21, 64, 64
+    g = torch.Generator("cuda").manual_seed(57)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")
+    pool, q = (r(pages, page, C + DR) * 0.5 + 1).bfloat16(), (r(B, H, 1, C + DR) * 0.01).bfloat16()
+    table = (torch.arange(n // page, device="cuda") % pages).to(torch.int32)
+    x, lse = ops.mla_prefix_decode(q[..., :C].contiguous(), q[..., C:].contiguous(), pool[..., :C], pool[..., C:], None,
+                                   None, 0.07, prefix_len=n, prefix_table=table)
+    k, qq = pool.flatten(0, 1).double(), q.double().reshape(B * H, -1)
+    want, want_lse, size = _attend(qq, k, 0.07)                  # every row as often: the same weights
+    at = 576 * 2.0 ** -24 * (qq.abs() @ k.abs().T).amax(1) * 0.07
+    tol = HALF * (size + want.abs()) + (2.0 ** 14 * 2.0 ** -23 + 2 * at[:, None]) * size
+    err = (x.double().reshape(B * H, C) - want).abs()
+    assert (err <= tol).all(), f"{(err / size).max().item():.2e} of the values"
+    want_lse = want_lse + math.log(n / len(k))
+    assert ((lse.double().reshape(-1) - want_lse).abs() <= at + 2.0 ** 14 * 2.0 ** -24 + 2.0 ** -22 * want_lse).all()
