@@ -27,6 +27,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmla.so")
 STEP_SRC = os.path.join(CSRC, "step_binding.cpp")
 STEP = os.path.join(PKG, "_step.so")
+STEP_STAMP = os.path.join(BUILD, "step.built_for")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -77,11 +78,23 @@ def build(force: bool = False, verbose: bool = False, build_binding: bool = True
     return LIB
 
 
+def built_for() -> str:
+    """What _step.so is compiled against, beside its source: torch's C++ classes and Python's C API."""
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
 def build_step(force: bool = False, verbose: bool = False) -> str:
-    """The C++ binding of the serving-step calls (needs libmla.so)."""
+    """The C++ binding of the serving-step calls (needs libmla.so).
+
+    Built anew when its source or mla.h is newer, or when it was built for another
+    torch or Python; the module carries what it was built for as ``built_for``.
+    """
     header = os.path.join(ROOT, "include", "mla.h")
     newest = max(os.path.getmtime(STEP_SRC), os.path.getmtime(header))
-    if not force and os.path.exists(STEP) and os.path.getmtime(STEP) >= newest:
+    here = built_for()
+    last = open(STEP_STAMP).read() if os.path.exists(STEP_STAMP) else None
+    if not force and last == here and os.path.exists(STEP) and os.path.getmtime(STEP) >= newest:
         return STEP
     import torch
     tdir = os.path.dirname(os.path.abspath(torch.__file__))
@@ -89,7 +102,7 @@ def build_step(force: bool = False, verbose: bool = False) -> str:
            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
     tmp = STEP + ".tmp"
     cmd = ([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [x for d in inc for x in ("-isystem", d)] +
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DSTEP_BUILT_FOR="{here}"'] + [x for d in inc for x in ("-isystem", d)] +
            [STEP_SRC, "-o", tmp, "-L" + PKG, "-l:" + os.path.basename(LIB), "-L" + os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
             "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + os.path.join(tdir, "lib")])
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -98,6 +111,9 @@ def build_step(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         sys.stderr.write(r.stderr)
     os.replace(tmp, STEP)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(STEP_STAMP, "w") as f:
+        f.write(here)
     return STEP
 
 

@@ -502,6 +502,7 @@ Tensor fp4_group_wo(const Tensor& x_given, const Tensor& wo_a, const OptTensor& 
 }  // namespace
 
 PYBIND11_MODULE(_step, m) {
+  m.attr("built_for") = STEP_BUILT_FOR;          // the torch and Python it was compiled against
   // the package's own error class, set by ops.py when it loads the module
   static py::object* error = nullptr;
   m.def("set_error", [](py::object cls) {

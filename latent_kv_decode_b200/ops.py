@@ -513,9 +513,16 @@ def _step():
         lib()
         if not os.path.exists(STEP_PATH):
             raise MlaError(f"{STEP_PATH} is missing; build it with `python -m latent_kv_decode_b200.build`")
-        spec = importlib.util.spec_from_file_location("_step", STEP_PATH)
-        mod = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(mod)
+        from .build import built_for
+        again = "build it anew with `python -m latent_kv_decode_b200.build`"
+        try:
+            spec = importlib.util.spec_from_file_location("_step", STEP_PATH)
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+        except ImportError as e:
+            raise MlaError(f"{STEP_PATH} does not load ({e}); {again}") from e
+        if mod.built_for != built_for():
+            raise MlaError(f"{STEP_PATH} was built for {mod.built_for}, this is {built_for()}; {again}")
         mod.set_error(MlaError)
         _step_mod = mod
     return _step_mod
