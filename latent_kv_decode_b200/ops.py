@@ -34,6 +34,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import math
 import os
 from dataclasses import dataclass, field
 from typing import Optional
@@ -613,6 +614,7 @@ def mla_prefix_decode_step(q_nope, q_pe, prefix_kv, prefix_pe, kv_cache, pe_cach
 
 
 FP4_BLOCK, FP4_ENTRY_BYTES = 512, 288
+_F32_TINY, _F32_MAX = torch.finfo(torch.float32).tiny, torch.finfo(torch.float32).max
 
 
 def pack_fp4_weight(w: torch.Tensor, scale: Optional[float] = None):
@@ -621,7 +623,7 @@ def pack_fp4_weight(w: torch.Tensor, scale: Optional[float] = None):
     ``w / scale`` is quantised by mla_cache_append's FP4 rule (an E4M3 scale per
     16 channels, E2M1 codes), so W ~ scale * value. Without ``scale`` it is chosen
     so that the largest weight meets the format's end (448 * 6); that reads the
-    maximum back to the host. Done once, when weights are loaded, on the current
+    maximum back to the host, and weights must be finite. Done once, when weights are loaded, on the current
     stream.
     """
     _need_cuda(w)
@@ -630,7 +632,12 @@ def pack_fp4_weight(w: torch.Tensor, scale: Optional[float] = None):
     with torch.cuda.device(w.device):
         wf = w.float()
         if scale is None:
-            scale = float(wf.abs().max()) / (448.0 * 6.0) or 1.0
+            top = float(wf.abs().max())
+            if not math.isfinite(top):
+                raise MlaError("pack_fp4_weight: weights must be finite")
+            scale = max(top / (448.0 * 6.0), _F32_TINY) if top else 1.0
+        if not _F32_TINY <= abs(scale) <= _F32_MAX:
+            raise MlaError("pack_fp4_weight: scale must be a normal float32")
         rows = (wf / scale).reshape(1, -1, FP4_BLOCK).contiguous()
         n = rows.shape[1]
         entries = torch.empty((1, n, FP4_ENTRY_BYTES), dtype=torch.uint8, device=w.device)
