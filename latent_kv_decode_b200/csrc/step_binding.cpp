@@ -440,7 +440,8 @@ Tensor linear_on(const Call& call, const Tensor& x, const Tensor& w, double scal
   const OptTensor wo(w);
   same_device(x, {&wo, &out_given, &err_flag});
   need(x.scalar_type() == at::kBFloat16, "mla_fp4_linear takes bf16 activations");
-  need(x.dim() >= 1 && w.dim() == 3 && x.size(-1) == w.size(1) * kBlock, "mla_fp4_linear: w must be (N, K/512, 288) for x (..., K)");
+  need(x.dim() >= 1 && w.dim() == 3 && w.size(1) > 0 && x.size(-1) == w.size(1) * kBlock,
+       "mla_fp4_linear: w must be (N, K/512, 288) for x (..., K)");
   const int64_t K = x.size(-1), N = w.size(0);
   std::vector<int64_t> shape = x.sizes().vec();
   shape.back() = N;

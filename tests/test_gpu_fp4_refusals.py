@@ -1,4 +1,5 @@
-"""Weights that no FP4 product can stand for are refused where they are packed."""
+"""Weights that no FP4 product can stand for are refused where they are packed, and products
+without channels before anything is computed."""
 import math
 
 import pytest
@@ -37,3 +38,16 @@ def test_weights_of_any_size(size):
     # in units of scale), x and y exact but for y's rounding to bf16
     tol = (2.0 ** -4 + 2.0 ** -7) * size + 6 * 2.0 ** -9 * scale + 2.0 ** -133
     assert ((y - w[:, 7].double()).abs() <= tol).all()
+
+
+def test_products_without_channels():
+    from latent_kv_decode_b200 import ops
+    x = torch.zeros((2, 0), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((3, 0, 288), dtype=torch.uint8, device="cuda")
+    with pytest.raises(ops.MlaError):
+        ops.mla_fp4_linear(x, w)
+    with pytest.raises(ops.MlaError):
+        ops.mla_fp4_linear(x.view(2, 1, 0), w)
+    x = torch.zeros((2, 0, 1, 512), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ops.MlaError):
+        ops.mla_fp4_group_wo(x, torch.zeros((0, 8, 1, 288), dtype=torch.uint8, device="cuda"))
