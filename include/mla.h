@@ -424,11 +424,16 @@ mla_status_t mla_rope_append(const mla_rope_append_args* a, void* stream);
  *     anything, NaN included.
  *   sinks: as for mla_decode.
  *   Supported: MLA_F32 or MLA_BF16; Ckv = 512; Dr 0, 32 or 64; H a multiple of 8
- *     up to 128, Q 1..4; B*H*Q up to 2^24, prefix_len + Lk up to 2^30. bf16 with
- *     contiguous storage or pages of a multiple of 64 rows runs at the tensor
- *     cores' full rate; everything else in float32 precision (six products of
- *     bf16 parts each).
- *   num_splits: 0 = auto; each block of stacked rows cuts its tokens into this
+ *     up to 128, Q 1..4; B*H*Q up to 2^24, prefix_len + Lk up to 2^30.
+ *   Precision: MLA_F32 in float32's (a product is six of bf16 parts). MLA_BF16:
+ *     exact products, float32 sums and statistics; for x the softmax weights
+ *     are rounded to bf16 (at most 2^-8 of a weight, of either sign; lse uses
+ *     them unrounded), with pages of other than a multiple of 64 rows to
+ *     2^-16. bf16 with contiguous storage or pages of a multiple of 64 rows runs
+ *     at the tensor cores' full rate; there x of a range loses about 2^-23 of
+ *     itself per 16 tokens to truncation, 0.0008 behind 2^17 tokens.
+ *   num_splits: 0 = auto (as many as fill the GPU, and for bf16 at least one per
+ *     2^18 tokens); each block of stacked rows cuts its tokens into this
  *     many ranges, and the call then merges the partial results itself (no
  *     mla_combine): x and lse are final when the enqueued work completes.
  *   workspace: mla_prefix_decode_workspace_size(a) bytes, 256-byte aligned

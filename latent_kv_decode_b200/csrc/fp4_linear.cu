@@ -14,8 +14,8 @@
 // first kernel scales each token's row by a power of two that brings its
 // largest finite magnitude to [2^14, 2^15) and stores it as float16. bf16 values
 // keep their 8 bits down to 2^-29 of that magnitude, and below it the error is
-// under 2^-40 of it, far below float32's accumulation. The epilogue takes the
-// power of two out again.
+// at most 2^-39 of it (half of float16's smallest step), far below float32's
+// accumulation. The epilogue takes the power of two out again.
 //
 //   x_to_f16      one CTA per (token, group): largest magnitude, then the row.
 //   fp4_linear    one cluster of S CTAs per 128 or 256 output rows and 64 tokens,
@@ -32,7 +32,8 @@
 // 16384 to 7168, 64 tokens, 30.7 us. With few tokens an MMA takes 24 ns whatever
 // its N (128 of them per CTA), behind 4 us for launch, activations and first entries
 // and before 2 us of exchange. With 64, the tokens' tiles are as many bytes as the
-// weights, and a GPC takes in about 0.87 TB/s from L2.
+// weights (130 MB come into 112 SMs together, 4.1 TB/s), and no pipe is full: issue slots
+// 59%, logic 46%, tensor 34% of the active cycles on average, 84, 61 and 45 on the busiest SM.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>

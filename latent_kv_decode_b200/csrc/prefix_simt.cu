@@ -11,13 +11,13 @@
 // The products are mma.m16n8k16 on bf16 parts: a float32 value is the sum of three
 // bf16, exactly (down to their smallest, 2^-133), and of the nine products of two such
 // sums the six largest count (the others are below 2^-25 of the first). With bf16 inputs
-// a score is one product, and a weight, a float32, two parts (to 2^-18 of it). The
+// a score is one product, and a weight, a float32, two parts (to 2^-16 of it). The
 // instruction adds in float32 and truncates, so what it adds up is kept short: a warp's
 // part of a score is at most 30 such additions, a tile's share of O six; parts and
 // tiles are added by rounding instructions. Behind 131072 tokens in one range x is
 // then within 7e-6 where O in the instruction's accumulator had lost 1e-3 of it. Q is
 // split once per CTA, K and V as their fragments are read, the weights by the softmax.
-// Measured: 4.1 us a tile (S 1.5, softmax 0.8, O 1.1), where packed float32 FMAs, which
+// Measured: 4.2 us a tile (S 1.5, softmax 0.8, O 1.2), where packed float32 FMAs, which
 // shared memory feeds with 32 floats a clock, took 5.4; 128 rows behind 2049 tokens 39
 // -> 31 us. (The warp-level instruction, as its operands come from registers, split
 // there; for tcgen05 the parts would have to be written to shared memory in its layout.)
@@ -531,7 +531,7 @@ cudaError_t launch(const PrefixParams& p, cudaStream_t st) {
 }  // namespace
 
 // About one CTA per SM (its shared memory fills one), no split shorter than a
-// tile: a tile takes 4.1 us, the merge of a few splits 3.
+// tile: a tile takes 4.2 us, the merge of a few splits 3.
 int prefix_simt_auto_splits(const mla_prefix_args* a, int sms) {
   const int HQ = a->H * a->Q;
   const int64_t rows = (int64_t)a->B * HQ;

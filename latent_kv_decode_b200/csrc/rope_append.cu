@@ -14,7 +14,7 @@
 // three float operations per rotated element, so what counts is bytes in flight.
 // A unit issues all its 16-byte loads (4 KB a warp) before the chain of
 // dependent lookups (token -> sequence -> length -> page) and the sine, and needs
-// no block barrier. 12,241 tokens, 128 heads: 69 us, 6.2 TB/s; with one CTA per token
+// no block barrier. 12,241 tokens, 128 heads: 68 to 69 us, 6.2 TB/s; with one CTA per token
 // and the loads behind the chain 85 us, with them before it in 70 registers 169 us.
 #include <cuda_bf16.h>
 #include <math.h>

@@ -1,6 +1,6 @@
 """mla_prefix_decode at the ends of its range, against the formula in 64 bits: token
-counts beyond 32 bits, long prefixes, sinks of -inf, rows that reach back into the
-prefix, references that move.
+counts beyond 32 bits, long prefixes, sinks and scores of -inf, causal rows that end
+before the prefix does.
 """
 import math
 
