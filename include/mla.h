@@ -433,8 +433,9 @@ mla_status_t mla_rope_append(const mla_rope_append_args* a, void* stream);
  *     at the tensor cores' full rate; there x of a range loses about 2^-23 of
  *     itself per 16 tokens to truncation, 0.0008 behind 2^17 tokens.
  *   num_splits: 0 = auto (as many as fill the GPU, and for bf16 at least one per
- *     2^18 tokens); each block of stacked rows cuts its tokens into this
- *     many ranges, and the call then merges the partial results itself (no
+ *     2^18 tokens; num_splits reports the most that the storage can ask for, a
+ *     block uses what its lengths ask for). Each block of stacked rows cuts its
+ *     tokens into this many ranges, and the call then merges the partial results itself (no
  *     mla_combine): x and lse are final when the enqueued work completes.
  *   workspace: mla_prefix_decode_workspace_size(a) bytes, 256-byte aligned
  *     (may be NULL when that is 0). It is written before it is read in every call;

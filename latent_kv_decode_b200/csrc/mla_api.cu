@@ -498,35 +498,45 @@ mla_status_t validate_prefix(const mla_prefix_args* a) {
   return MLA_OK;
 }
 
-int prefix_splits(const mla_prefix_args* a) {
+// Ranges of a launch; `wanted` as the kernels' rules give it (0: their number is given).
+int prefix_splits(const mla_prefix_args* a, int* wanted) {
+  *wanted = 0;
   if (a->num_splits > 0) return a->num_splits;
-  return mla::prefix_sm100_supported(a) ? mla::prefix_sm100_auto_splits(a, sm_count())
-                                        : mla::prefix_simt_auto_splits(a, sm_count());
+  return mla::prefix_sm100_supported(a) ? mla::prefix_sm100_auto_splits(a, sm_count(), wanted)
+                                        : mla::prefix_simt_auto_splits(a, sm_count(), wanted);
 }
 
 size_t prefix_ws_o_bytes(const mla_prefix_args* a, int S) {
   return ((size_t)S * a->B * a->H * a->Q * a->Ckv * sizeof(float) + 255) & ~(size_t)255;
 }
 
+size_t prefix_ws_lse_bytes(const mla_prefix_args* a, int S) { return (size_t)S * a->B * a->H * a->Q * sizeof(float); }
+
+// partial outputs, their log-sum-exps and, unless the count is given, each block's
 size_t prefix_ws_bytes(const mla_prefix_args* a, int S) {
-  return S <= 1 ? 0 : prefix_ws_o_bytes(a, S) + (size_t)S * a->B * a->H * a->Q * sizeof(float);
+  if (S <= 1) return 0;
+  const size_t rows = (size_t)a->B * a->H * a->Q, blocks = ((rows - 1) >> mla::kPrefixLeastShift) + 1;
+  return prefix_ws_o_bytes(a, S) + prefix_ws_lse_bytes(a, S) + (a->num_splits > 0 ? 0 : blocks * sizeof(int32_t));
 }
 
 }  // namespace
 
 extern "C" int mla_prefix_decode_num_splits(const mla_prefix_args* a) {
-  return validate_prefix(a) != MLA_OK ? -1 : prefix_splits(a);
+  int wanted;
+  return validate_prefix(a) != MLA_OK ? -1 : prefix_splits(a, &wanted);
 }
 
 extern "C" size_t mla_prefix_decode_workspace_size(const mla_prefix_args* a) {
-  return validate_prefix(a) != MLA_OK ? 0 : prefix_ws_bytes(a, prefix_splits(a));
+  int wanted;
+  return validate_prefix(a) != MLA_OK ? 0 : prefix_ws_bytes(a, prefix_splits(a, &wanted));
 }
 
 extern "C" mla_status_t mla_prefix_decode(const mla_prefix_args* a, void* workspace, size_t workspace_bytes,
                                           void* stream) {
   mla_status_t s = validate_prefix(a);
   if (s != MLA_OK) return s;
-  const int S = prefix_splits(a);
+  int wanted;
+  const int S = prefix_splits(a, &wanted);
   const size_t need = prefix_ws_bytes(a, S);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return MLA_ERR_WORKSPACE;
   mla::PrefixParams p;
@@ -565,16 +575,20 @@ extern "C" mla_status_t mla_prefix_decode(const mla_prefix_args* a, void* worksp
   p.scale = a->softmax_scale;
   p.sinks = a->sinks;
   p.num_splits = S;
+  p.wanted = wanted;
   p.x = a->x;
   p.lse = a->lse;
   p.err = a->err_flag;
   if (S > 1) {
     p.ws_o = (float*)workspace;
     p.ws_lse = (float*)((char*)workspace + prefix_ws_o_bytes(a, S));
+    if (wanted > 0) p.ws_ranges = (int32_t*)((char*)p.ws_lse + prefix_ws_lse_bytes(a, S));
   }
   cudaStream_t st = (cudaStream_t)stream;
   const bool bf16 = a->dtype == MLA_BF16;
-  s = cuda_status(mla::prefix_sm100_supported(a) ? mla::launch_prefix_sm100(p, st) : mla::launch_prefix_simt(p, bf16, st));
+  const bool sm100 = mla::prefix_sm100_supported(a);
+  p.block_shift = sm100 ? mla::kPrefixMostShift : mla::kPrefixLeastShift;
+  s = cuda_status(sm100 ? mla::launch_prefix_sm100(p, st) : mla::launch_prefix_simt(p, bf16, st));
   if (s != MLA_OK || S == 1) return s;
   return cuda_status(mla::launch_prefix_combine(p, bf16, st));
 }

@@ -32,12 +32,15 @@ struct PrefixParams {
   int causal;
   float scale;
   const float* sinks;
-  int num_splits;
+  int num_splits;                   // ranges of a block at the most: those of the launch
+  int wanted;                       // ranges that fill the GPU (with ws_ranges)
+  int block_shift;                  // log2 of a block's rows
   void* x;
   float* lse;
   int32_t* err;
   float* ws_o;                      // (S, N, Ckv) normalised partial outputs
   float* ws_lse;                    // (S, N)
+  int32_t* ws_ranges;               // (blocks) ranges that a block used, or null: num_splits
 };
 
 __device__ __forceinline__ void prefix_flag(const PrefixParams& p, int bit) {
@@ -98,6 +101,33 @@ struct TileWalk {
   }
 };
 
+// How a block cuts its tiles. The launch counts own tokens as the storage allows, the
+// block as they are: with the launch's count, 4 sequences of 8 heads, 256 + up to 500
+// tokens took 23 us with a table for 131072 tokens, 15 now, and 13 with one for 512.
+struct Cut {
+  int per;                          // tiles of a range
+  bool several;                     // the outputs are partial ones
+  bool idle;                        // this range is not used: nothing to write, nothing reads it
+};
+
+// Range z of a block of `tiles`, none of more than `most` if the launch has that many.
+__device__ __forceinline__ Cut prefix_cut(const PrefixParams& p, int tiles, int most, int z) {
+  const int n = max(tiles, 1);
+  int s = p.num_splits;
+  if (p.ws_ranges) s = min(max(min(p.wanted, n), (n - 1) / most + 1), s);
+  Cut c;
+  c.per = (n + s - 1) / s;
+  c.several = p.ws_ranges ? c.per < n : s > 1;
+  c.idle = p.ws_ranges && z * c.per >= n;
+  return c;
+}
+
+// The ranges that a block uses, for the merge.
+__device__ __forceinline__ void prefix_tell(const PrefixParams& p, int block, int tiles, const Cut& c) {
+  if (p.ws_ranges) p.ws_ranges[block] = (max(tiles, 1) + c.per - 1) / c.per;
+}
+
+constexpr int kPrefixLeastShift = 5, kPrefixMostShift = 7;   // log2 of a block's rows: prefix_simt, prefix_sm100
 constexpr int kPrefixMaxSplits = 256;   // ranges of a block that the merge holds the weights of
 
 // At most s ranges (1 if less), as few as keep the longest as short: ranges that
@@ -109,10 +139,19 @@ inline int even_splits(int64_t tiles, int64_t s) {
 }
 
 cudaError_t launch_prefix_simt(const PrefixParams& p, bool bf16, cudaStream_t st);
-int prefix_simt_auto_splits(const mla_prefix_args* a, int sms);
+// Should the blocks cut their tiles by the lengths that they have? Not where these are
+// the storage's, nor where own tokens, as the storage allows them, are few of the tiles:
+// the merge then waits for one load less (13.0 : 13.3 us, 31.2 : 31.8 for small calls).
+inline bool prefix_cut_by_lengths(const mla_prefix_args* a, int64_t own, int64_t tiles) {
+  return a->seq_lens && own > 8 && own > tiles / 8;
+}
+
+// Ranges of a launch; `wanted`: how many fill the GPU, where the blocks cut by their
+// lengths, else 0.
+int prefix_simt_auto_splits(const mla_prefix_args* a, int sms, int* wanted);
 
 bool prefix_sm100_supported(const mla_prefix_args* a);
-int prefix_sm100_auto_splits(const mla_prefix_args* a, int sms);
+int prefix_sm100_auto_splits(const mla_prefix_args* a, int sms, int* wanted);
 cudaError_t launch_prefix_sm100(const PrefixParams& p, cudaStream_t st);
 
 // merges the split partials in p.ws_o / p.ws_lse into p.x / p.lse

@@ -1,7 +1,7 @@
 // Merge of the split partials of the shared-prefix decode:
 //   L = log(sum_s e^{lse_s} [+ e^{sink}]),  x = sum_s e^{lse_s - L} O_s.
 // A split that saw nothing of a row has lse = -inf and O = 0 (every row of every
-// split is written); a NaN lse (a non-finite input the row sees) makes the row NaN.
+// split that the row's block uses is written); a NaN lse (a non-finite input the row sees) makes the row NaN.
 //
 // A row's lse values are reduced across a warp's lanes, which keep the splits' weights
 // and hand them round. With many rows, one warp per row fills the GPU: each lane owns
@@ -14,8 +14,9 @@
 namespace mla {
 namespace {
 
-// kQuarters: parts of a row's columns, kShare: ranges of its splits, a warp each.
-template <typename T, int kQuarters, int kShare>
+// kQuarters: parts of a row's columns, kShare: ranges of its splits, a warp each. kAsks:
+// the blocks said how many splits they used.
+template <typename T, int kQuarters, int kShare, bool kAsks>
 __global__ void __launch_bounds__(kQuarters* kShare > 1 ? 32 * kQuarters * kShare : 128)
     prefix_combine(const PrefixParams p) {
   constexpr bool kRowPerCta = kQuarters * kShare > 1;
@@ -27,7 +28,8 @@ __global__ void __launch_bounds__(kQuarters* kShare > 1 ? 32 * kQuarters * kShar
   sm100::pdl_launch_dependents();
   sm100::pdl_wait();
   if (r >= p.N) return;                          // whole warp; with a row per CTA never
-  const int S = p.num_splits;
+  int S = p.num_splits;
+  if constexpr (kAsks) S = min(S, p.ws_ranges[r >> p.block_shift]);
   const float sink = p.sinks ? p.sinks[(int)(r % p.HQ) / p.Q] : -INFINITY;
   float m = sink, w[kHeld];
   bool nan = false;
@@ -35,10 +37,12 @@ __global__ void __launch_bounds__(kQuarters* kShare > 1 ? 32 * kQuarters * kShar
   for (int k = 0; k < kHeld; ++k) {
     const int s = lane + 32 * k;
     w[k] = -INFINITY;
-    if (s < S) w[k] = p.ws_lse[(int64_t)s * p.N + r];
+    if (s < p.num_splits) w[k] = p.ws_lse[(int64_t)s * p.N + r];   // all, not behind the load of S
+    if constexpr (kAsks) w[k] = s < S ? w[k] : -INFINITY;
     nan = nan || isnan(w[k]);
     m = fmaxf(m, w[k]);
   }
+  if (kAsks && S == 1) return;                   // the row is final (the same for the row's warps)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   nan = __any_sync(0xffffffffu, nan);
@@ -138,7 +142,8 @@ cudaError_t launch(const PrefixParams& p, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefix_combine<T, kQuarters, kShare>, p);
+  return p.ws_ranges ? cudaLaunchKernelEx(&cfg, prefix_combine<T, kQuarters, kShare, true>, p)
+                     : cudaLaunchKernelEx(&cfg, prefix_combine<T, kQuarters, kShare, false>, p);
 }
 
 }  // namespace

@@ -34,7 +34,7 @@
 namespace mla {
 namespace {
 
-constexpr int kRows = 32, kToks = 16;
+constexpr int kRows = 1 << kPrefixLeastShift, kToks = 16;
 constexpr int kThr = 256, kWarps = kThr / 32, kParts = kWarps;   // kParts slices of the dot product
 constexpr int kPad = 8;             // floats of row padding: four rows x eight floats cover the banks
 constexpr int kPart = kToks + 1;
@@ -163,7 +163,10 @@ template <typename T> __device__ __forceinline__ void decode_range(const PrefixP
   if (tid <= b1 - b0) lens[tid] = prefix_len_of(p, b0 + tid);
   __syncthreads();
   const int tiles = TileWalk<kToks>::count(p, lens, b0, b1);
-  const int per = (tiles + p.num_splits - 1) / p.num_splits;
+  const Cut cut = prefix_cut(p, tiles, 0x7fffffff, z);
+  if (tid == 0 && z == 0) prefix_tell(p, blockIdx.x, tiles, cut);
+  if (cut.idle) return;
+  const int per = cut.per;
   const int j0 = min(tiles, z * per), j1 = min(tiles, j0 + per);
 
   // the rows of tile `w` into buffer s (after a barrier that follows its last use)
@@ -437,7 +440,7 @@ template <typename T> __device__ __forceinline__ void decode_range(const PrefixP
   }
 
   // the rows' denominators to the accumulator's threads
-  const bool parts = p.num_splits > 1;
+  const bool parts = cut.several;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -532,13 +535,16 @@ cudaError_t launch(const PrefixParams& p, cudaStream_t st) {
 
 // About one CTA per SM (its shared memory fills one), no split shorter than a
 // tile: a tile takes 4.2 us, the merge of a few splits 3.
-int prefix_simt_auto_splits(const mla_prefix_args* a, int sms) {
+int prefix_simt_auto_splits(const mla_prefix_args* a, int sms, int* wanted) {
   const int HQ = a->H * a->Q;
   const int64_t rows = (int64_t)a->B * HQ;
   const int64_t blocks = (rows + kRows - 1) / kRows;
   const int64_t seqs = std::min<int64_t>(a->B, (kRows + HQ - 1) / HQ);   // of a block
-  const int64_t tiles = ((int64_t)a->prefix_len + kToks - 1) / kToks + seqs * ((a->Lk + kToks - 1) / kToks);
-  return even_splits(tiles, std::min({sms / blocks, tiles, (int64_t)64}));
+  const int64_t own = seqs * ((a->Lk + kToks - 1) / kToks);
+  const int64_t tiles = ((int64_t)a->prefix_len + kToks - 1) / kToks + own;
+  const int64_t fill = std::max<int64_t>(std::min({sms / blocks, tiles, (int64_t)64}), 1);
+  *wanted = prefix_cut_by_lengths(a, own, tiles) ? (int)fill : 0;
+  return even_splits(tiles, fill);
 }
 
 cudaError_t launch_prefix_simt(const PrefixParams& p, bool bf16, cudaStream_t st) {

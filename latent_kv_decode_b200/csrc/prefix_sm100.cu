@@ -76,7 +76,7 @@ constexpr int kSoft = 128 * kSets;          // softmax threads (warps 4 and up)
 constexpr int kSoftWarps = kSoft / 32;
 constexpr int kThreads = 128 + kSoft;
 constexpr int kTileT = 128;                 // tokens per tile (both CTAs)
-constexpr int kRowsT = 128;                 // stacked rows per cluster
+constexpr int kRowsT = 1 << kPrefixMostShift;     // stacked rows per cluster
 constexpr int kChunk = 8192;                // 64 rows (tokens or query rows) x 128 B
 
 constexpr int kOffQ = 0;                    // 9 chunks: q_lat 0-7, q_pe
@@ -109,7 +109,8 @@ constexpr int kOffAbort = kOffTmemPtr + 4;
 constexpr int kOffFlags = (kOffAbort + 4 + 15) & ~15;     // int [2 tiles][16 warps of the peer]
 constexpr int kMaxSeqs = kRowsT / 8 + 1;                  // H*Q >= 8: the sequences a block can hold rows of
 constexpr int kOffLens = kOffFlags + 2 * kSoftWarps * 4;  // int [kMaxSeqs]: their own lengths
-constexpr int kCtrlBytes = (kOffLens + kMaxSeqs * 4 + 15) & ~15;
+constexpr int kOffCut = kOffLens + kMaxSeqs * 4;         // int: bit 0 several ranges, bit 1 idle
+constexpr int kCtrlBytes = (kOffCut + 4 + 15) & ~15;
 constexpr int kOffXmax = kBigBytes;                       // float [sets][128 lanes]
 constexpr int kOffAlpha = kOffXmax + 512 * kSets;                // float [128]
 constexpr int kOffScl = kOffAlpha + 512;                  // float [128]
@@ -124,6 +125,7 @@ constexpr uint32_t kTmemCols = 512;
 
 constexpr int kTok = 64 / kSets;            // scores of a tile per softmax thread
 constexpr uint32_t kAll = 0xffffffffu >> (32 - kTok);
+constexpr int kMostTiles = 2048;            // of a range, 2^18 tokens (prefix_sm100_auto_splits)
 constexpr float kMove = 60.0f;              // log2: how far a score may exceed its row's reference
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -314,9 +316,10 @@ __global__ void __maxnreg__(96) prefix_sm100_kernel(const __grid_constant__ TcPa
   }
   __syncthreads();
   const int tiles = TileWalk<kTileT>::count(p, lens, b0, b1);
-  const int per = (tiles + p.num_splits - 1) / p.num_splits;
-  const int j_begin = min(tiles, z * per);
-  const int ntiles = __shfl_sync(0xffffffffu, min(tiles, j_begin + per) - j_begin, 0);
+  const Cut cut = prefix_cut(p, tiles, kMostTiles, z);
+  if (z == 0 && rank == 0 && threadIdx.x == 0) prefix_tell(p, rb, tiles, cut);
+  const int j_begin = min(tiles, z * cut.per);
+  const int ntiles = __shfl_sync(0xffffffffu, min(tiles, j_begin + cut.per) - j_begin, 0);
   TileWalk<kTileT> w;
   w.seek(p, lens, b0, b1, j_begin);
 
@@ -541,6 +544,9 @@ __global__ void __maxnreg__(96) prefix_sm100_kernel(const __grid_constant__ TcPa
     // the last token a causal row sees, as a position (own token 0 is at Lp)
     const int last_pos = !live ? -1 : p.causal ? p.Lp + lens[my_b - b0] - p.Q + r % p.Q : 0x3fffffff;
 
+    // kept in shared memory over the loop, whose registers are counted
+    volatile int* cut_s = reinterpret_cast<volatile int*>(ctrl_p + kOffCut);
+    if (leader) *cut_s = (cut.several ? 1 : 0) | (cut.idle ? 2 : 0);
     const bool look = bar_or(1, kSoft, bad_pages(p, lens, b0, b1, j_begin, ntiles, xi, kSoft));
     const int to_all = seen_by_all(p, lens, b0, b1, lane);
 
@@ -720,7 +726,8 @@ __global__ void __maxnreg__(96) prefix_sm100_kernel(const __grid_constant__ TcPa
     // the rows' denominators, then each row's output scale to both CTAs
     ab = bar_or(1, kSoft, ab);
     const float l_tot = across(l_part, [](float a, float b) { return a + b; });
-    const bool split = p.num_splits > 1;
+    const int cut_bits = *cut_s;
+    const bool split = cut_bits & 1, idle = cut_bits & 2;
     const bool seen = !(m_run == -INFINITY && l_tot == 0.f);   // a NaN denominator stays one
     float scale_o = seen ? 1.f / l_tot : 0.f;
     float lse = seen ? (m_run + log2f(l_tot)) * kLn2 : -INFINITY;
@@ -738,7 +745,7 @@ __global__ void __maxnreg__(96) prefix_sm100_kernel(const __grid_constant__ TcPa
     if (owner) {
       scl[col] = scale_o;
       st_async_b32(map_to_rank(smem_u32(scl + col), peer), __float_as_uint(scale_o), map_to_rank(bar(B_EPX), peer));
-      if (live) {
+      if (live && !idle) {
         if (split)
           p.ws_lse[(int64_t)z * p.N + r] = lse;
         else if (p.lse)
@@ -760,7 +767,7 @@ __global__ void __maxnreg__(96) prefix_sm100_kernel(const __grid_constant__ TcPa
     const int n = sset;                                      // set n stores half n
     const int d0 = 256 * n + 128 * (int)rank + 32 * g;       // this warp's first dim
 #pragma unroll 1
-    for (int c0 = 0; c0 < kRowsT && r0 + c0 < p.N; c0 += 16) {
+    for (int c0 = 0; c0 < kRowsT && r0 + c0 < p.N && !idle; c0 += 16) {
       uint32_t v[16];
       if (have_o) {
         tmem_ld16(tmem + lane_base + kColO + 128u * n + (uint32_t)c0, v);
@@ -874,19 +881,22 @@ bool prefix_sm100_supported(const mla_prefix_args* a) {
 }
 
 // As many clusters as run at once, but no range shorter than a tile of the blocks' most
-// (own tokens counted as the storage allows, their lengths being on the device): down to
-// one tile a range the merge costs less than the tiles it spares (16 sequences of 8
+// (own tokens counted as the storage allows, their lengths being on the device, where
+// a block then takes the ranges that it needs): down to one tile a range the merge costs less than the tiles it spares (16 sequences of 8
 // heads, 500 + 100 tokens: 43, 22, 16 us with 1, 5, 20 ranges). And no range much above
 // 2^18 tokens: the tensor pipe adds to O once per 16 tokens and truncates, which takes
 // more of x the longer the range (behind 2^17, 2^20, 2^22 tokens of equal weight 0.0008,
 // 0.006 and 0.024 of it, where a rounding to bf16 takes at most 0.0039).
-int prefix_sm100_auto_splits(const mla_prefix_args* a, int sms) {
+int prefix_sm100_auto_splits(const mla_prefix_args* a, int sms, int* wanted) {
   const int pairs = sms / 2, HQ = a->H * a->Q;
   const int64_t blocks = ((int64_t)a->B * HQ + kRowsT - 1) / kRowsT;
   const int64_t seqs = std::min<int64_t>(a->B, (kRowsT + HQ - 1) / HQ);   // of a block
-  const int64_t tiles = ((int64_t)a->prefix_len + kTileT - 1) / kTileT + seqs * ((a->Lk + kTileT - 1) / kTileT);
+  const int64_t own = seqs * ((a->Lk + kTileT - 1) / kTileT);
+  const int64_t tiles = ((int64_t)a->prefix_len + kTileT - 1) / kTileT + own;
   const int64_t least = std::min<int64_t>(((int64_t)a->prefix_len + a->Lk + (1 << 18) - 1) >> 18, kPrefixMaxSplits);
-  return even_splits(tiles, std::max(std::min(pairs / blocks, tiles), least));
+  const int64_t fill = std::max<int64_t>(std::min(pairs / blocks, tiles), 1);
+  *wanted = prefix_cut_by_lengths(a, own, tiles) ? (int)fill : 0;
+  return even_splits(tiles, std::max(fill, least));
 }
 
 cudaError_t launch_prefix_sm100(const PrefixParams& p, cudaStream_t st) {

@@ -249,3 +249,87 @@ def test_bf16_sums_over_two_million_tokens(H, B):
     assert (err <= tol).all(), f"{(err / size).max().item():.2e} of the values"
     want_lse = want_lse + math.log(n / len(k))
     assert ((lse.double().reshape(-1) - want_lse).abs() <= at + 2.0 ** 14 * 2.0 ** -24 + 2.0 ** -22 * want_lse).all()
+
+
+@pytest.mark.parametrize("dtype,page", [(torch.float32, 64), (torch.bfloat16, 64), (torch.bfloat16, 16)])
+@pytest.mark.parametrize("B,H,Lp,longest", [(4, 8, 256, 500), (4, 16, 100, 3), (3, 128, 700, 130), (40, 128, 300, 200)])
+def test_tables_that_allow_more_than_the_lengths_use(B, H, Lp, longest, dtype, page):
+    # a block takes the ranges that its lengths ask for, whatever the table allows, and the
+    # others leave nothing behind. Some sequences are empty, and the tables' other entries
+    # are no pages
+    from latent_kv_decode_b200 import ops
+    g = torch.Generator("cuda").manual_seed(58)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(dtype)
+    lens = [longest * (b % 4) // 3 for b in range(B)]
+    n, per = -(-Lp // page), -(-longest // page)
+    pool, q_lat, q_pe = r(n + B * per, page, C + DR), r(B, H, 1, C), r(B, H, 1, DR)
+    tight = torch.arange(n, n + B * per, dtype=torch.int32, device="cuda").view(B, per)
+    prefix_table = torch.arange(n, dtype=torch.int32, device="cuda")
+
+    def call(capacity, **kw):
+        table = torch.full((B, capacity // page), -1, dtype=torch.int32, device="cuda")
+        table[:, :per] = tight
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        ws = ops.make_prefix_decode(q_lat, q_pe, pool[..., :C], pool[..., C:], pool[..., :C], pool[..., C:], 0.07,
+                                    prefix_len=Lp, prefix_table=prefix_table, page_size=page, block_table=table,
+                                    seq_lens=torch.tensor(lens, dtype=torch.int32, device="cuda"), err_flag=err, **kw)
+        if ws.workspace is not None:
+            ws.workspace.fill_(0x7F)                     # what is not written this time must not be read
+        ws.x.fill_(math.nan)
+        ws.lse.fill_(math.nan)
+        x, lse = ops.launch_prefix_decode(ws)
+        assert int(err.item()) == 0
+        return x, lse
+
+    half = HALF if dtype == torch.bfloat16 else 0
+    oracle = {}
+    for b in {0, 1, 2, 3 % B, B - 1}:
+        k = torch.cat([pool[:n].flatten(0, 1)[:Lp], pool[n + b * per:n + (b + 1) * per].flatten(0, 1)[:lens[b]]]).double()
+        q = torch.cat([q_lat[b, :, 0], q_pe[b, :, 0]], -1).double()
+        at = 576 * 2.0 ** -24 * (q.abs() @ k.abs().T).amax(1) * 0.07
+        oracle[b] = (*_attend(q, k, 0.07), at)
+    for capacity in (per * page, 131072, 2 ** 19):
+        x, lse = call(capacity)
+        assert torch.isfinite(x).all() and torch.isfinite(lse).all()
+        for b, (want, want_lse, size, at) in oracle.items():
+            # roundings to bf16; float32 sums and exponentials of a few hundred tokens
+            tol = half * (size + want.abs()) + (2 * at[:, None] + 2.0 ** -15) * size
+            assert ((x[b, :, 0].double() - want).abs() <= tol).all(), f"capacity {capacity}, sequence {b}"
+            assert ((lse[b, :, 0].double() - want_lse).abs() <= at + 2.0 ** -15).all()
+
+
+@pytest.mark.parametrize("dtype,page", [(torch.float32, 64), (torch.bfloat16, 64), (torch.bfloat16, 16)])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_empty_sequences_with_large_tables(dtype, page, sinks):
+    # blocks without a token beside blocks with some: one range each, or several, in one call
+    from latent_kv_decode_b200 import ops
+    B, H, capacity = 24, 16, 65536
+    g = torch.Generator("cuda").manual_seed(59)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(dtype)
+    lens = [0] * 16 + [0, 700, 1, 0, 64, 0, 0, 130]
+    pool, q_lat, q_pe = r(44 * 64 // page, page, C + DR), r(B, H, 1, C), r(B, H, 1, DR)
+    table = torch.full((B, capacity // page), -1, dtype=torch.int32, device="cuda")
+    used = 0
+    rows = {}
+    for b, n in enumerate(lens):
+        need = -(-n // page)
+        table[b, :need] = torch.arange(used, used + need, device="cuda")
+        rows[b] = pool[used:used + need].flatten(0, 1)[:n].double()
+        used += need
+    sink = torch.randn(H, generator=g, device="cuda") if sinks else None
+    x, lse = ops.mla_prefix_decode(q_lat, q_pe, None, None, pool[..., :C], pool[..., C:], 0.07, block_table=table,
+                                   page_size=page, seq_lens=torch.tensor(lens, dtype=torch.int32, device="cuda"), sinks=sink)
+    for b, n in enumerate(lens):
+        if n == 0:
+            assert (x[b] == 0).all()
+            want = sink if sinks else torch.full((H,), -math.inf, device="cuda")
+            # e^(sink - sink) and its logarithm, or log2 and back: float32 on either way
+            assert torch.allclose(lse[b, :, 0], want, rtol=2.0 ** -21, atol=2.0 ** -21)
+            continue
+        q = torch.cat([q_lat[b, :, 0], q_pe[b, :, 0]], -1).double()
+        want, want_lse, size = _attend(q, rows[b], 0.07, sink.double() if sinks else None)
+        at = 576 * 2.0 ** -24 * (q.abs() @ rows[b].abs().T).amax(1) * 0.07
+        half = HALF if dtype == torch.bfloat16 else 0
+        tol = half * (size + want.abs()) + (2 * at[:, None] + 2.0 ** -15) * size
+        assert ((x[b, :, 0].double() - want).abs() <= tol).all(), f"sequence {b}"
+        assert ((lse[b, :, 0].double() - want_lse).abs() <= at + 2.0 ** -15).all()
