@@ -33,7 +33,7 @@
 // its N (128 of them per CTA), behind 4 us for launch, activations and first entries
 // and before 2 us of exchange. With 64, the tokens' tiles are as many bytes as the
 // weights (130 MB come into 112 SMs together, 4.1 TB/s), and no pipe is full: issue slots
-// 59%, logic 46%, tensor 34% of the active cycles on average, 84, 61 and 45 on the busiest SM.
+// 59%, logic 46%, tensor 34% of the active cycles on average, 83, 61 and 45 on the busiest SM.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>

@@ -43,12 +43,12 @@
 // than one of the prefix (64 x 128 heads, 4096 tokens: 79 us as own ones, 63 as a prefix).
 //
 // A tile's 17 + 16 MMA steps of K = 64 take about 2870 SM cycles in the tensor
-// pipe (1.46 us); a tile takes 1.53 us in a small GPC and 1.65 to 1.7 with all 74
+// pipe (1.46 us); a tile takes 1.53 us in a small GPC and 1.65 to 1.74 with all 74
 // clusters busy, 1.5 to 1.6 PFLOP/s by the device, where the power limit (1.42 for a long
 // library product) comes into sight. Not loading the other CTA's tokens at all (32 of
 // 104 KB a tile) gains 2%. Measured (whole call, merge included): 128 sequences of 16
-// heads x 2 queries behind 16384 tokens 153 us, 64 of 128 heads behind 4096 tokens 76 us,
-// 4 of 128 heads behind 131072 tokens 142 us: 0.97, 1.03 and 1.03 PFLOP/s, with 64, 64
+// heads x 2 queries behind 16384 tokens 157 us, 64 of 128 heads behind 4096 tokens 77 us,
+// 4 of 128 heads behind 131072 tokens 145 us: 0.94, 1.00 and 1.01 PFLOP/s, with 64, 64
 // and 72 clusters.
 //
 // Warps (384 threads): 0 own-token producer, 1 QK issuer (CTA 0) and TMEM
