@@ -333,3 +333,40 @@ def test_empty_sequences_with_large_tables(dtype, page, sinks):
         tol = half * (size + want.abs()) + (2 * at[:, None] + 2.0 ** -15) * size
         assert ((x[b, :, 0].double() - want).abs() <= tol).all(), f"sequence {b}"
         assert ((lse[b, :, 0].double() - want_lse).abs() <= at + 2.0 ** -15).all()
+
+
+@pytest.mark.parametrize("dtype,page", [(torch.float32, 64), (torch.bfloat16, 64), (torch.bfloat16, 16)])
+def test_a_captured_call_follows_its_lengths(dtype, page):
+    # the ranges are cut on the device: one graph, replayed while sequences grow from nothing
+    # to several tiles, gives the eager call's bits
+    from latent_kv_decode_b200 import ops
+    B, H, Lp, capacity = 6, 16, 100, 32768
+    g = torch.Generator("cuda").manual_seed(60)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(dtype)
+    pages = 1024 // page
+    pool, q_lat, q_pe = r(B * pages + 128 // page, page, C + DR), r(B, H, 1, C), r(B, H, 1, DR)
+    table = torch.full((B, capacity // page), -1, dtype=torch.int32, device="cuda")
+    table[:, :pages] = torch.arange(B * pages, device="cuda").view(B, pages)
+    prefix_table = torch.arange(B * pages, B * pages + 128 // page, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    call = lambda: ops.mla_prefix_decode(q_lat, q_pe, pool[..., :C], pool[..., C:], pool[..., :C], pool[..., C:], 0.07,
+                                         prefix_len=Lp, prefix_table=prefix_table, page_size=page, block_table=table,
+                                         seq_lens=lens)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x, lse = call()
+    for step in ([0] * 6, [1, 0, 2, 0, 0, 3], [1024, 1, 130, 0, 700, 64], [0, 0, 0, 0, 0, 1], [1024] * 6):
+        lens.copy_(torch.tensor(step, dtype=torch.int32))
+        graph.replay()
+        want, want_lse = call()
+        torch.cuda.synchronize()
+        assert torch.equal(x, want) and torch.equal(lse, want_lse), str(step)
+        for b in range(B):
+            k = torch.cat([pool[prefix_table.long()].flatten(0, 1)[:Lp], pool[table[b, :pages].long()].flatten(0, 1)[:step[b]]]).double()
+            q = torch.cat([q_lat[b, :, 0], q_pe[b, :, 0]], -1).double()
+            v, _, size = _attend(q, k, 0.07)
+            at = 576 * 2.0 ** -24 * (q.abs() @ k.abs().T).amax(1) * 0.07
+            half = HALF if dtype == torch.bfloat16 else 0
+            assert ((x[b, :, 0].double() - v).abs() <= half * (size + v.abs()) + (2 * at[:, None] + 2.0 ** -15) * size).all()
